@@ -258,8 +258,10 @@ def _norm_rope_plain(s):
 def _norm_rope_own(s):
     import block_sparse_attention_dense_b200 as lf
     case = s["case"]
-    desc = lf.make_qk_desc(s["q"], s["k"], s["qw"], s["kw"], s["cos_sin"], cu_seqlens=s["cu"],
-                           positions=s["positions"], eps=EPS, interleaved=case["interleaved"])
+    if "desc" not in s:   # the layer's descriptor, kept from step to step
+        s["desc"] = lf.make_qk_desc(s["q"], s["k"], s["qw"], s["kw"], s["cos_sin"], cu_seqlens=s["cu"],
+                                    positions=s["positions"], eps=EPS, interleaved=case["interleaved"])
+    desc = s["desc"]
     if case["op"] == "norm_rope":
         lf.lf_qk_norm_rope(desc, s["q"], s["k"], s["q_out"], s["k_out"])
         return s["q_out"], s["k_out"]
