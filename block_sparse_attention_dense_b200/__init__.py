@@ -5,8 +5,8 @@ liblazyflash.so.  PyTorch provides device memory and streams.  There is no CPU
 fallback: importing the binding without the built library raises.
 
 Functions keep the C names: lf_attn_fwd, lf_block_select, lf_attn_bwd,
-lf_workspace_size, lf_sync_status (alias lf_check_device_error),
-lf_status_string.  Tensors are torch
+lf_workspace_size, lf_qk_norm_rope, lf_qk_norm_rope_bwd, lf_qk_workspace_size,
+lf_sync_status (alias lf_check_device_error), lf_status_string.  Tensors are torch
 CUDA tensors in the layouts the header states; the stream defaults to torch's
 current stream.
 """
@@ -26,7 +26,10 @@ LF_SELECT_NORMS_GIVEN = 0x1
 LF_RULE_BUDGET, LF_RULE_FIXED_FRACTION, LF_RULE_TOPK = 0, 1, 2
 
 EXPORTED = ("lf_workspace_size", "lf_attn_fwd", "lf_block_select", "lf_attn_bwd",
+            "lf_qk_norm_rope", "lf_qk_norm_rope_bwd", "lf_qk_workspace_size",
             "lf_sync_status", "lf_check_device_error", "lf_status_string")
+LF_ROPE_HALVES, LF_ROPE_PAIRS = 0, 1
+LF_QK_NORM, LF_QK_ZERO_TAIL = 0x1, 0x2
 
 
 class LfError(RuntimeError):
@@ -47,6 +50,27 @@ class lf_attn_desc(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("causal", ctypes.c_int32),
         ("block_q", ctypes.c_int32),
+    ]
+
+
+class lf_qk_desc(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("nseq", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("cos_sin", ctypes.c_void_p),
+        ("npos", ctypes.c_int32),
+        ("rot", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("weights_bf16", ctypes.c_int32),
     ]
 
 
@@ -79,6 +103,13 @@ def _load():
     L.lf_check_device_error.restype = i32
     L.lf_sync_status.argtypes = [vp]
     L.lf_sync_status.restype = i32
+    i64, qptr = ctypes.c_int64, ctypes.POINTER(lf_qk_desc)
+    L.lf_qk_norm_rope.argtypes = [qptr] + [vp, i64] * 4 + [vp]
+    L.lf_qk_norm_rope.restype = i32
+    L.lf_qk_workspace_size.argtypes = [qptr, ctypes.POINTER(sz)]
+    L.lf_qk_workspace_size.restype = i32
+    L.lf_qk_norm_rope_bwd.argtypes = [qptr] + [vp, i64] * 6 + [vp, vp, vp, sz, vp]
+    L.lf_qk_norm_rope_bwd.restype = i32
     _lib = L
     return L
 
@@ -233,3 +264,107 @@ def lf_attn_bwd_static_ws(desc, q, k, v, o, lse, dout, D, block_weight, kept_idx
     _check(fn(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout),
               _ptr(D), _ptr(block_weight), _ptr(kept_idx), _ptr(kept_cnt), _ptr(dq), _ptr(dk),
               _ptr(dv), _stream(stream)), "lf_attn_bwd_static_ws")
+
+
+# --------------------------------------------------------------------------------------
+# norms of the query and key heads with the position rotation
+# --------------------------------------------------------------------------------------
+def _on_device(device, call, stream):
+    """call(stream pointer) with `device` current, on torch's current stream of that
+    device unless a stream is given."""
+    if torch.cuda.current_device() == device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _vector(t, name, device, dtypes, numel=None):
+    """Checks a contiguous device array; returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on %s" % (
+            name, " or ".join(str(d).replace("torch.", "") for d in dtypes), device))
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, not %d" % (name, numel, t.numel()))
+    return t.data_ptr()
+
+
+def rope_cos_sin(npos: int, rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Table of lf_qk_norm_rope: fp32 [npos, rot], row p the cosines, then the sines, of
+    p * theta^(-2i/rot), i < rot/2.  The angles are computed in 64 bits, so that far
+    positions keep theirs."""
+    inv = theta ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    a = torch.arange(npos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def make_qk_desc(q, k, q_weight=None, k_weight=None, cos_sin=None, cu_seqlens=None, positions=None,
+                 eps: float = 1e-6, norm: bool = True, interleaved: bool = False,
+                 zero_tail: bool = False) -> lf_qk_desc:
+    """Descriptor of lf_qk_norm_rope for q [T, hq, d] and k [T, hkv, d] (only their sizes
+    and device are taken).  Weights [d] bf16 or fp32, both of one type, or None for ones;
+    cos_sin [npos, rot] fp32 (see rope_cos_sin) or None for no rotation; cu_seqlens and
+    positions int32.  The descriptor keeps the tensors it points to."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError("q and k must be [T, heads, d] with the same T and d")
+    if not q.is_cuda or k.device != q.device:
+        raise ValueError("q and k must be CUDA tensors on one device")
+    T, hq, d = q.shape
+    ws = [w for w in (q_weight, k_weight) if w is not None]
+    if len({w.dtype for w in ws}) > 1:
+        raise ValueError("q_weight and k_weight must have one type")
+    dev = q.device
+    floats = (torch.bfloat16, torch.float32)
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [npos, rot]")
+    desc = lf_qk_desc(
+        T, hq, k.shape[1], d, 0 if cu_seqlens is None else cu_seqlens.numel() - 1,
+        _vector(cu_seqlens, "cu_seqlens", dev, (torch.int32,)),
+        _vector(positions, "positions", dev, (torch.int32,), T),
+        _vector(cos_sin, "cos_sin", dev, (torch.float32,)),
+        0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
+        LF_ROPE_PAIRS if interleaved else LF_ROPE_HALVES,
+        (LF_QK_NORM if norm else 0) | (LF_QK_ZERO_TAIL if zero_tail else 0), float(eps),
+        _vector(q_weight, "q_weight", dev, floats, d), _vector(k_weight, "k_weight", dev, floats, d),
+        int(bool(ws) and ws[0].dtype == torch.bfloat16))
+    desc._keepalive = (q_weight, k_weight, cos_sin, cu_seqlens, positions)
+    desc._device = dev
+    return desc
+
+
+def _rows(t, desc, heads, name):
+    """Address and token stride of a [T, heads, d] bf16 operand whose heads are contiguous."""
+    T, d = desc.total_tokens, desc.d
+    if t.dtype != torch.bfloat16 or t.device != desc._device or tuple(t.shape) != (T, heads, d):
+        raise ValueError("%s must be a bf16 [%d, %d, %d] tensor on %s" % (name, T, heads, d, desc._device))
+    s = t.stride()
+    if T and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        raise ValueError("%s must have contiguous heads" % name)
+    return t.data_ptr(), (s[0] if T > 1 else heads * d)
+
+
+def lf_qk_workspace_size(desc: lf_qk_desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_load().lf_qk_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "lf_qk_workspace_size")
+    return n.value
+
+
+def lf_qk_norm_rope(desc, q, k, q_out, k_out, stream=None):
+    args = (*_rows(q, desc, desc.hq, "q"), *_rows(k, desc, desc.hkv, "k"),
+            *_rows(q_out, desc, desc.hq, "q_out"), *_rows(k_out, desc, desc.hkv, "k_out"))
+    _check(_on_device(desc._device, lambda s: _load().lf_qk_norm_rope(ctypes.byref(desc), *args, s),
+                      stream), "lf_qk_norm_rope")
+
+
+def lf_qk_norm_rope_bwd(desc, q, k, dq_out, dk_out, dq, dk, dqw=None, dkw=None, ws=None, stream=None):
+    f32 = (torch.float32,)
+    none = (None, 0)
+    args = (*(none if q is None else _rows(q, desc, desc.hq, "q")),
+            *(none if k is None else _rows(k, desc, desc.hkv, "k")),
+            *_rows(dq_out, desc, desc.hq, "dq_out"), *_rows(dk_out, desc, desc.hkv, "dk_out"),
+            *_rows(dq, desc, desc.hq, "dq"), *_rows(dk, desc, desc.hkv, "dk"),
+            _vector(dqw, "dqw", desc._device, f32, desc.d), _vector(dkw, "dkw", desc._device, f32, desc.d),
+            _vector(ws, "ws", desc._device, (torch.uint8,)), 0 if ws is None else ws.numel())
+    _check(_on_device(desc._device, lambda s: _load().lf_qk_norm_rope_bwd(ctypes.byref(desc), *args, s),
+                      stream), "lf_qk_norm_rope_bwd")

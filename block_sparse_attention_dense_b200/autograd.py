@@ -1,4 +1,5 @@
-"""LazyFlash as a torch.autograd.Function (argument marshalling only).
+"""LazyFlash, and the norms and rotation before it, as torch.autograd.Functions
+(argument marshalling only).
 
 The forward is the exact dense attention (lf_attn_fwd); the backward selects
 query blocks from the incoming output gradient (lf_block_select: budget delta,
@@ -18,7 +19,8 @@ import math
 
 import torch
 
-from . import (Buffers, lf_attn_bwd, lf_attn_fwd, lf_block_select, make_desc)
+from . import (Buffers, lf_attn_bwd, lf_attn_fwd, lf_block_select, lf_qk_norm_rope,
+               lf_qk_norm_rope_bwd, lf_qk_workspace_size, make_desc, make_qk_desc)
 
 _step_counter = itertools.count()
 
@@ -73,3 +75,53 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     device tensors), ``kept_cnt`` and the Philox ``step`` used."""
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
                                     block_q, softmax_scale, selection_out)
+
+
+class QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos_sin, cu_seqlens, positions, eps, norm, interleaved):
+        # rows behind the last segment (a padded batch) come out as zeros, and so do their
+        # gradients: every element of what this returns is defined
+        desc = make_qk_desc(q, k, q_weight, k_weight, cos_sin, cu_seqlens, positions, eps, norm,
+                            interleaved, zero_tail=True)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        lf_qk_norm_rope(desc, q, k, q_out, k_out)
+        # without the norm the gradient does not read the inputs
+        ctx.save_for_backward(*((q, k) if norm else (None, None)), q_weight, k_weight, cos_sin,
+                              cu_seqlens, positions)
+        ctx.desc = desc
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        q, k, q_weight, k_weight = ctx.saved_tensors[:4]
+        desc = ctx.desc
+        gq = gq.to(torch.bfloat16).contiguous()
+        gk = gk.to(torch.bfloat16).contiguous()
+        dq, dk = torch.empty_like(gq), torch.empty_like(gk)
+
+        def grad_of(w, needed):
+            return torch.empty(desc.d, dtype=torch.float32, device=gq.device) if w is not None and needed else None
+
+        dqw = grad_of(q_weight, ctx.needs_input_grad[2])
+        dkw = grad_of(k_weight, ctx.needs_input_grad[3])
+        ws = None
+        if dqw is not None or dkw is not None:
+            ws = torch.empty(lf_qk_workspace_size(desc), dtype=torch.uint8, device=gq.device)
+        lf_qk_norm_rope_bwd(desc, q, k, gq, gk, dq, dk, dqw, dkw, ws)
+        return (dq, dk, None if dqw is None else dqw.to(q_weight.dtype),
+                None if dkw is None else dkw.to(k_weight.dtype), None, None, None, None, None, None)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos_sin=None, cu_seqlens=None, positions=None,
+                 eps=1e-6, norm=True, interleaved=False):
+    """RMS norm of every query and key head, then the position rotation, in one pass; both
+    differentiable (see lf_qk_norm_rope in include/lazyflash.h).
+
+    q [T, hq, d], k [T, hkv, d] bf16; they may be slices of one fused projection's output
+    (contiguous heads, any token stride).  The results are contiguous and go into
+    lazyflash_attention.  cos_sin: rope_cos_sin(npos, rot), or None for the norm alone;
+    norm=False rotates only.  A row's position is its index in its segment of cu_seqlens,
+    or positions[row]."""
+    return QkNormRope.apply(q, k, q_weight, k_weight, cos_sin, cu_seqlens, positions, eps, norm, interleaved)

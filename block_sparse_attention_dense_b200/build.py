@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblazyflash.so")
 SOURCES = ["lazyflash.cu"]
-HEADERS = ["lf_device.cuh", "lf_select.cuh", "lf_fwd.cuh", "lf_bwd.cuh"]
+HEADERS = ["lf_device.cuh", "lf_select.cuh", "lf_fwd.cuh", "lf_bwd.cuh", "lf_qknorm.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

@@ -1,19 +1,22 @@
 // Host side of the LazyFlash C ABI (include/lazyflash.h): argument checks,
 // workspace sizing, TMA tensor-map encoding and kernel launches.  Nothing
 // here computes attention; every step of the path runs in the kernels of
-// lf_fwd.cuh, lf_select.cuh and lf_bwd.cuh.
+// lf_fwd.cuh, lf_select.cuh, lf_bwd.cuh and lf_qknorm.cuh.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "lazyflash.h"
 #include "lf_bwd.cuh"
 #include "lf_device.cuh"
 #include "lf_fwd.cuh"
+#include "lf_qknorm.cuh"
 #include "lf_select.cuh"
 
 namespace {
@@ -272,6 +275,87 @@ lf_status launch_bwd(const lf_attn_desc* d, const void* q, const void* k, const 
                                                    static_cast<uint4*>(dv), nkv8, 1.0f);
     }
     return launch_status();
+}
+
+lf_status check_qk_desc(const lf_qk_desc* d) {
+    if (!d) return LF_ERR_INVALID_ARG;
+    if (d->total_tokens < 0 || d->hq < 1 || d->hkv < 1 || d->rot < 0) return LF_ERR_INVALID_ARG;
+    if (d->d != 64 && d->d != 128) return LF_ERR_UNSUPPORTED;
+    if (d->hq > 65535 || d->hkv > 65535) return LF_ERR_UNSUPPORTED;
+    if (d->cu_seqlens && d->nseq < 1) return LF_ERR_INVALID_ARG;
+    if (d->rot > d->d) return LF_ERR_INVALID_ARG;
+    if (d->rot % 16 != 0) return LF_ERR_UNSUPPORTED;
+    if (d->rot > 0 && (!d->cos_sin || d->npos < 1 || (!d->positions && !d->cu_seqlens)))
+        return LF_ERR_INVALID_ARG;
+    if (d->pairing != LF_ROPE_HALVES && d->pairing != LF_ROPE_PAIRS) return LF_ERR_INVALID_ARG;
+    if (d->flags & ~(LF_QK_NORM | LF_QK_ZERO_TAIL)) return LF_ERR_INVALID_ARG;
+    if (d->flags & LF_QK_NORM) {
+        if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return LF_ERR_INVALID_ARG;
+        if (d->weights_bf16 != 0 && d->weights_bf16 != 1) return LF_ERR_INVALID_ARG;
+        if (!aligned16(d->q_weight) || !aligned16(d->k_weight)) return LF_ERR_INVALID_ARG;
+    } else if (d->q_weight || d->k_weight || d->rot == 0) {
+        return LF_ERR_INVALID_ARG;   // weights without the norm; or nothing to do
+    }
+    if (!aligned16(d->cos_sin)) return LF_ERR_INVALID_ARG;
+    return LF_OK;
+}
+
+// A strided [T][heads][d] bf16 operand.
+bool qk_operand_ok(const lf_qk_desc* d, const void* p, int64_t stride, int heads) {
+    return p && aligned16(p) && stride % 8 == 0 && stride >= (int64_t)heads * d->d;
+}
+
+lf::QkParams qk_params(const lf_qk_desc* d) {
+    lf::QkParams p{};
+    p.T = d->total_tokens;
+    p.hq = d->hq;
+    p.hkv = d->hkv;
+    p.nseq = d->nseq;
+    p.npos = d->npos;
+    p.rot = d->rot;
+    p.weights_bf16 = d->weights_bf16;
+    p.zero_tail = (d->flags & LF_QK_ZERO_TAIL) ? 1 : 0;
+    p.cu = d->cu_seqlens;
+    p.positions = d->positions;
+    p.cos_sin = d->cos_sin;
+    p.eps = d->eps;
+    p.qw = d->q_weight;
+    p.kw = d->k_weight;
+    return p;
+}
+
+// The grid over units of row groups (see lf_qknorm.cuh).  A warp takes a token's whole
+// list of row groups once there are tokens enough to give every SM 16 warps; with fewer
+// tokens the list is cut so that the warps of the whole GPU share it.  Returns the blocks.
+int qk_grid(const lf_qk_desc* d, lf::QkParams& p) {
+    const int rpw = 32 / (d->d / 8);
+    const int ng = (d->hq + rpw - 1) / rpw + (d->hkv + rpw - 1) / rpw;
+    const long long cut = std::min<long long>(ng, (148ll * 16 + p.T - 1) / p.T);
+    p.per_unit = static_cast<int>((ng + cut - 1) / cut);
+    p.units_per_token = (ng + p.per_unit - 1) / p.per_unit;
+    const long long units = (long long)p.T * p.units_per_token;
+    return static_cast<int>(std::min<long long>((units + 7) / 8, lf::kQkMaxBlocks));
+}
+
+template <int D, bool kNorm, bool kPairs>
+lf_status launch_qk(const lf::QkParams& p, int blocks, bool bwd, cudaStream_t st) {
+    if (bwd)
+        lf::qk_norm_rope_bwd_kernel<D, kNorm, kPairs><<<blocks, lf::kQkThreads, 0, st>>>(p);
+    else
+        lf::qk_norm_rope_kernel<D, kNorm, kPairs><<<blocks, lf::kQkThreads, 0, st>>>(p);
+    return launch_status();
+}
+
+lf_status launch_qk_any(const lf_qk_desc* d, const lf::QkParams& p, int blocks, bool bwd,
+                        cudaStream_t st) {
+    const bool norm = (d->flags & LF_QK_NORM) != 0, pairs = d->pairing == LF_ROPE_PAIRS;
+    auto by_d = [&](auto n, auto pr) {
+        constexpr bool N = decltype(n)::value, P = decltype(pr)::value;
+        return d->d == 128 ? launch_qk<128, N, P>(p, blocks, bwd, st)
+                           : launch_qk<64, N, P>(p, blocks, bwd, st);
+    };
+    if (norm) return pairs ? by_d(std::true_type{}, std::true_type{}) : by_d(std::true_type{}, std::false_type{});
+    return pairs ? by_d(std::false_type{}, std::true_type{}) : by_d(std::false_type{}, std::false_type{});
 }
 
 }  // namespace
@@ -553,6 +637,95 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
                                        : launch_bwd<64>(desc, q, k, v, o, lse, dout, D, block_weight,
                                                         kept_idx, kept_cnt, dq, dk, dv, ws, s),
                         s);
+}
+
+lf_status lf_qk_norm_rope(const lf_qk_desc* desc, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, lf_stream_t stream) {
+    lf_status st = check_qk_desc(desc);
+    if (st != LF_OK) return st;
+    if (desc->total_tokens == 0) return pending_device_error();
+    if (!qk_operand_ok(desc, q, q_stride, desc->hq) || !qk_operand_ok(desc, k, k_stride, desc->hkv) ||
+        !qk_operand_ok(desc, q_out, q_out_stride, desc->hq) ||
+        !qk_operand_ok(desc, k_out, k_out_stride, desc->hkv))
+        return LF_ERR_INVALID_ARG;
+    if ((st = pending_device_error()) != LF_OK) return st;
+    if ((st = prepare_device()) != LF_OK) return st;
+    lf::QkParams p = qk_params(desc);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.qs = q_stride;
+    p.ks = k_stride;
+    p.oq = static_cast<__nv_bfloat16*>(q_out);
+    p.ok = static_cast<__nv_bfloat16*>(k_out);
+    p.oqs = q_out_stride;
+    p.oks = k_out_stride;
+    const int blocks = qk_grid(desc, p);
+    return launch_qk_any(desc, p, blocks, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_qk_workspace_size(const lf_qk_desc* desc, size_t* bytes) {
+    lf_status st = check_qk_desc(desc);
+    if (st != LF_OK) return st;
+    if (!bytes) return LF_ERR_INVALID_ARG;
+    *bytes = (size_t)lf::kQkMaxBlocks * 2 * desc->d * sizeof(float);
+    return LF_OK;
+}
+
+lf_status lf_qk_norm_rope_bwd(const lf_qk_desc* desc, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* dq_out,
+                              int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride,
+                              void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                              float* dqw, float* dkw, void* ws, size_t ws_bytes,
+                              lf_stream_t stream) {
+    lf_status st = check_qk_desc(desc);
+    if (st != LF_OK) return st;
+    const bool norm = (desc->flags & LF_QK_NORM) != 0, weights = dqw || dkw;
+    if (weights && !norm) return LF_ERR_INVALID_ARG;
+    const bool rows = desc->total_tokens > 0;
+    if (rows && norm &&
+        (!qk_operand_ok(desc, q, q_stride, desc->hq) || !qk_operand_ok(desc, k, k_stride, desc->hkv)))
+        return LF_ERR_INVALID_ARG;
+    if (rows && (!qk_operand_ok(desc, dq_out, dq_out_stride, desc->hq) ||
+                 !qk_operand_ok(desc, dk_out, dk_out_stride, desc->hkv) ||
+                 !qk_operand_ok(desc, dq, dq_stride, desc->hq) ||
+                 !qk_operand_ok(desc, dk, dk_stride, desc->hkv)))
+        return LF_ERR_INVALID_ARG;
+    if (!aligned16(dqw) || !aligned16(dkw) || !aligned16(ws)) return LF_ERR_INVALID_ARG;
+    if ((st = pending_device_error()) != LF_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!rows) {
+        const size_t b = desc->d * sizeof(float);
+        if ((dqw && cudaMemsetAsync(dqw, 0, b, s) != cudaSuccess) ||
+            (dkw && cudaMemsetAsync(dkw, 0, b, s) != cudaSuccess))
+            return LF_ERR_CUDA;
+        return LF_OK;
+    }
+    size_t need = 0;
+    if ((st = lf_qk_workspace_size(desc, &need)) != LF_OK) return st;
+    if (weights && (!ws || ws_bytes < need)) return LF_ERR_WORKSPACE;
+    if ((st = prepare_device()) != LF_OK) return st;
+    lf::QkParams p = qk_params(desc);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.qs = q_stride;
+    p.ks = k_stride;
+    p.gq = static_cast<const __nv_bfloat16*>(dq_out);
+    p.gk = static_cast<const __nv_bfloat16*>(dk_out);
+    p.gqs = dq_out_stride;
+    p.gks = dk_out_stride;
+    p.oq = static_cast<__nv_bfloat16*>(dq);
+    p.ok = static_cast<__nv_bfloat16*>(dk);
+    p.oqs = dq_stride;
+    p.oks = dk_stride;
+    p.partial = weights ? static_cast<float*>(ws) : nullptr;
+    const int blocks = qk_grid(desc, p);
+    if ((st = launch_qk_any(desc, p, blocks, true, s)) != LF_OK) return st;
+    if (weights) {
+        lf::qk_weight_grad_kernel<<<2 * desc->d / 32, dim3(32, 32), 0, s>>>(p.partial, blocks, desc->d, dqw, dkw);
+        return launch_status();
+    }
+    return LF_OK;
 }
 
 lf_status lf_watchdog_selftest(uint32_t limit_log2, lf_stream_t stream) {

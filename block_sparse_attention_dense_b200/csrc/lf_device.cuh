@@ -25,6 +25,8 @@ __device__ int* g_error_mirror;
 
 constexpr int kErrTimeout = 1;        // a bounded wait expired
 constexpr int kErrBadSegments = 2;    // cu_seqlens inconsistent with T / max_seqlen
+constexpr int kErrBadPosition = 3;    // a rotation position outside the table
+constexpr int kErrBadMask = 4;        // row_start or prefix_len breaks its rules
 
 constexpr long long kWaitLimitCycles = 1ll << 31;   // ~1.1 s at 1.9 GHz
 

@@ -219,6 +219,76 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
                                 const int32_t* kept_idx, const int32_t* kept_cnt, void* dq,
                                 void* dk, void* dv, lf_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms of the query and key heads with the position rotation (no counterpart in
+ * the article: the step between a layer's projections and its attention in models
+ * that normalise their heads, such as the article's).
+ *
+ *   n = w * x / sqrt(mean(x^2) + eps) over the d values of one head of one token
+ *   (n = x without LF_QK_NORM), then for every rotated pair (a, b) with angle
+ *   index i: y_a = n_a cos_i - n_b sin_i, y_b = n_b cos_i + n_a sin_i; columns at
+ *   or past `rot` are not rotated.  Computed in fp32 and rounded once to bf16.
+ * ------------------------------------------------------------------------- */
+
+/* Which columns of a head form pair i, i in [0, rot/2). */
+enum {
+    LF_ROPE_HALVES = 0,   /* (i, i + rot/2) */
+    LF_ROPE_PAIRS = 1     /* (2i, 2i + 1) */
+};
+
+/* Flags of lf_qk_desc. */
+#define LF_QK_NORM 0x1u        /* norm before the rotation */
+#define LF_QK_ZERO_TAIL 0x2u   /* rows behind the last segment are written as 0 instead of left as they are */
+
+typedef struct {
+    int32_t total_tokens;       /* T >= 0 */
+    int32_t hq, hkv, d;         /* heads of q and of k (any counts >= 1), head dim 64 or 128 */
+    int32_t nseq;               /* segments of cu_seqlens (ignored when it is NULL) */
+    const int32_t* cu_seqlens;  /* DEVICE [nseq + 1], or NULL.  Given, only rows below
+                                   cu_seqlens[nseq] are computed, and without `positions` a row's
+                                   position is its index in its segment */
+    const int32_t* positions;   /* DEVICE [T], or NULL.  rot > 0 needs positions or cu_seqlens */
+    const float* cos_sin;       /* DEVICE [npos][rot], row p: rot/2 cosines, then rot/2 sines, of the
+                                   angles of position p (NULL when rot = 0) */
+    int32_t npos;               /* rows of cos_sin */
+    int32_t rot;                /* rotated columns: 0 or a multiple of 16 up to d */
+    int32_t pairing;            /* LF_ROPE_HALVES or LF_ROPE_PAIRS */
+    uint32_t flags;             /* LF_QK_* */
+    float eps;                  /* >= 0, used with LF_QK_NORM */
+    const void* q_weight;       /* DEVICE [d] norm weights, or NULL for ones; only with LF_QK_NORM */
+    const void* k_weight;
+    int32_t weights_bf16;       /* 1: the weights are bf16; 0: fp32 */
+} lf_qk_desc;
+
+/* Forward.  q, k: bf16, token t at q + t * q_stride (elements), its heads [hq][d]
+ * contiguous, so that slices of one fused projection need no copy; q_out, k_out
+ * likewise.  A stride is a multiple of 8 elements and at least heads * d; pointers
+ * are 16-byte aligned.  Outputs may be the inputs (same pointer and stride); any
+ * other overlap is not allowed.  A position outside [0, npos) is a device-side
+ * failure (LF_ERR_INVALID_ARG from the next call); that row is not written.
+ * Row offsets are computed in 64 bits. */
+lf_status lf_qk_norm_rope(const lf_qk_desc* desc, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out,
+                          int64_t k_out_stride, lf_stream_t stream);
+
+/* Bytes of workspace lf_qk_norm_rope_bwd needs when it is asked for weight gradients. */
+lf_status lf_qk_workspace_size(const lf_qk_desc* desc, size_t* bytes);
+
+/* Gradient.  dq_out, dk_out: gradients of the forward's outputs; dq, dk: gradients of
+ * its inputs (bf16; each may be dq_out / dk_out or q / k itself).  dqw, dkw: fp32 [d]
+ * gradients of the norm weights, overwritten, summed over all computed rows and heads
+ * in a fixed order (the same inputs give the same bits); NULL where not wanted, and
+ * NULL without LF_QK_NORM.  q and k are read only with LF_QK_NORM (else they may be
+ * NULL).  ws is needed when dqw or dkw is given.  Rows that the forward leaves out
+ * get no gradient (0 with LF_QK_ZERO_TAIL, else left as they are) and add nothing to
+ * dqw and dkw. */
+lf_status lf_qk_norm_rope_bwd(const lf_qk_desc* desc, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* dq_out,
+                              int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride,
+                              void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                              float* dqw, float* dkw, void* ws, size_t ws_bytes,
+                              lf_stream_t stream);
+
 /* Failure-detection self-test (no counterpart in the article): launches one
  * CTA whose bounded barrier wait, the one every kernel uses, waits for a phase
  * that nothing completes and gives up after 2^limit_log2 SM cycles (10..31),
