@@ -327,22 +327,23 @@ lf::QkParams qk_params(const lf_qk_desc* d) {
 // The grid over units of row groups (see lf_qknorm.cuh).  A warp takes a token's whole
 // list of row groups once there are tokens enough to give every SM 16 warps; with fewer
 // tokens the list is cut so that the warps of the whole GPU share it.  Returns the blocks.
-int qk_grid(const lf_qk_desc* d, lf::QkParams& p) {
+int qk_grid(const lf_qk_desc* d, lf::QkParams& p, bool bwd) {
     const int rpw = 32 / (d->d / 8);
     const int ng = (d->hq + rpw - 1) / rpw + (d->hkv + rpw - 1) / rpw;
     const long long cut = std::min<long long>(ng, (148ll * 16 + p.T - 1) / p.T);
     p.per_unit = static_cast<int>((ng + cut - 1) / cut);
     p.units_per_token = (ng + p.per_unit - 1) / p.per_unit;
     const long long units = (long long)p.T * p.units_per_token;
-    return static_cast<int>(std::min<long long>((units + 7) / 8, lf::kQkMaxBlocks));
+    return static_cast<int>(
+        std::min<long long>((units + 7) / 8, 148 * (bwd ? lf::kQkBlocksBwd : lf::kQkBlocksFwd)));
 }
 
 template <int D, bool kNorm, bool kPairs>
 lf_status launch_qk(const lf::QkParams& p, int blocks, bool bwd, cudaStream_t st) {
     if (bwd)
-        lf::qk_norm_rope_bwd_kernel<D, kNorm, kPairs><<<blocks, lf::kQkThreads, 0, st>>>(p);
+        lf::qk_norm_rope_kernel<D, kNorm, kPairs, true><<<blocks, lf::kQkThreads, 0, st>>>(p);
     else
-        lf::qk_norm_rope_kernel<D, kNorm, kPairs><<<blocks, lf::kQkThreads, 0, st>>>(p);
+        lf::qk_norm_rope_kernel<D, kNorm, kPairs, false><<<blocks, lf::kQkThreads, 0, st>>>(p);
     return launch_status();
 }
 
@@ -660,7 +661,7 @@ lf_status lf_qk_norm_rope(const lf_qk_desc* desc, const void* q, int64_t q_strid
     p.ok = static_cast<__nv_bfloat16*>(k_out);
     p.oqs = q_out_stride;
     p.oks = k_out_stride;
-    const int blocks = qk_grid(desc, p);
+    const int blocks = qk_grid(desc, p, false);
     return launch_qk_any(desc, p, blocks, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -719,7 +720,7 @@ lf_status lf_qk_norm_rope_bwd(const lf_qk_desc* desc, const void* q, int64_t q_s
     p.oqs = dq_stride;
     p.oks = dk_stride;
     p.partial = weights ? static_cast<float*>(ws) : nullptr;
-    const int blocks = qk_grid(desc, p);
+    const int blocks = qk_grid(desc, p, true);
     if ((st = launch_qk_any(desc, p, blocks, true, s)) != LF_OK) return st;
     if (weights) {
         lf::qk_weight_grad_kernel<<<2 * desc->d / 32, dim3(32, 32), 0, s>>>(p.partial, blocks, desc->d, dqw, dkw);
