@@ -5,7 +5,7 @@ liblazyflash.so.  PyTorch provides device memory and streams.  There is no CPU
 fallback: importing the binding without the built library raises.
 
 Functions keep the C names: lf_attn_fwd, lf_block_select, lf_attn_bwd,
-lf_workspace_size, lf_qk_norm_rope, lf_qk_norm_rope_bwd, lf_qk_workspace_size,
+lf_workspace_size, lf_attn_fwd_mod, lf_attn_bwd_mod, lf_qk_norm_rope, lf_qk_norm_rope_bwd, lf_qk_workspace_size,
 lf_sync_status (alias lf_check_device_error), lf_status_string.  Tensors are torch
 CUDA tensors in the layouts the header states; the stream defaults to torch's
 current stream.
@@ -26,7 +26,7 @@ LF_SELECT_NORMS_GIVEN = 0x1
 LF_RULE_BUDGET, LF_RULE_FIXED_FRACTION, LF_RULE_TOPK = 0, 1, 2
 
 EXPORTED = ("lf_workspace_size", "lf_attn_fwd", "lf_block_select", "lf_attn_bwd",
-            "lf_qk_norm_rope", "lf_qk_norm_rope_bwd", "lf_qk_workspace_size",
+            "lf_attn_fwd_mod", "lf_attn_bwd_mod", "lf_qk_norm_rope", "lf_qk_norm_rope_bwd", "lf_qk_workspace_size",
             "lf_sync_status", "lf_check_device_error", "lf_status_string")
 LF_ROPE_HALVES, LF_ROPE_PAIRS = 0, 1
 LF_QK_NORM, LF_QK_ZERO_TAIL = 0x1, 0x2
@@ -50,6 +50,16 @@ class lf_attn_desc(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("causal", ctypes.c_int32),
         ("block_q", ctypes.c_int32),
+    ]
+
+
+class lf_score_mod(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p),
+        ("prefix_causal", ctypes.c_int32),
+        ("row_start", ctypes.c_void_p),
     ]
 
 
@@ -103,6 +113,11 @@ def _load():
     L.lf_check_device_error.restype = i32
     L.lf_sync_status.argtypes = [vp]
     L.lf_sync_status.restype = i32
+    mptr = ctypes.POINTER(lf_score_mod)
+    L.lf_attn_fwd_mod.argtypes = [dptr, mptr, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lf_attn_fwd_mod.restype = i32
+    L.lf_attn_bwd_mod.argtypes = [dptr, mptr] + [vp] * 14 + [sz, vp]
+    L.lf_attn_bwd_mod.restype = i32
     i64, qptr = ctypes.c_int64, ctypes.POINTER(lf_qk_desc)
     L.lf_qk_norm_rope.argtypes = [qptr] + [vp, i64] * 4 + [vp]
     L.lf_qk_norm_rope.restype = i32
@@ -266,9 +281,7 @@ def lf_attn_bwd_static_ws(desc, q, k, v, o, lse, dout, D, block_weight, kept_idx
               _ptr(dv), _stream(stream)), "lf_attn_bwd_static_ws")
 
 
-# --------------------------------------------------------------------------------------
-# norms of the query and key heads with the position rotation
-# --------------------------------------------------------------------------------------
+
 def _on_device(device, call, stream):
     """call(stream pointer) with `device` current, on torch's current stream of that
     device unless a stream is given."""
@@ -290,6 +303,101 @@ def _vector(t, name, device, dtypes, numel=None):
     return t.data_ptr()
 
 
+# --------------------------------------------------------------------------------------
+# attention with modified scores
+# --------------------------------------------------------------------------------------
+def make_score_mod(softcap: float = 0.0, alibi_slopes=None, prefix_len=None, prefix_causal: bool = False,
+                   row_start=None) -> lf_score_mod:
+    """Modifier of lf_attn_fwd_mod and lf_attn_bwd_mod (meaning: include/lazyflash.h).
+    alibi_slopes fp32 [hq], prefix_len int32 [nseq], row_start int32 [T]: CUDA tensors on
+    one device, which the modifier keeps."""
+    given = [t for t in (alibi_slopes, prefix_len, row_start) if t is not None]
+    dev = given[0].device if given else None
+    if dev is not None and dev.type != "cuda":
+        raise ValueError("the modifier's arrays must be CUDA tensors")
+    i32 = (torch.int32,)
+    mod = lf_score_mod(float(softcap), _vector(alibi_slopes, "alibi_slopes", dev, (torch.float32,)),
+                       _vector(prefix_len, "prefix_len", dev, i32), int(bool(prefix_causal)),
+                       _vector(row_start, "row_start", dev, i32))
+    mod._keepalive = (alibi_slopes, prefix_len, row_start)
+    mod._sizes = tuple(None if t is None else t.numel() for t in mod._keepalive)
+    mod._device = dev
+    return mod
+
+
+def _check_attention(desc, mod, q, k, v, rest=()):
+    """Types, shapes and devices of an attention call with modified scores; its device."""
+    T, d, dev = desc.total_tokens, desc.d, q.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    tokens = [("q", q, desc.hq), ("k", k, desc.hkv), ("v", v, desc.hkv)]
+    for name, t, heads in tokens + [r for r in rest if r[1] is not None and isinstance(r[2], int)]:
+        if t.dtype != torch.bfloat16 or t.device != dev or tuple(t.shape) != (T, heads, d) or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous bf16 [%d, %d, %d] tensor on %s" % (name, T, heads, d, dev))
+    for name, t, want in rest:
+        if t is not None and not isinstance(want, int):
+            dtype, numel = want
+            _vector(t, name, dev, (dtype,), numel)
+    keep = getattr(desc, "_keepalive", None)
+    if (keep is not None and keep.device != dev) or (mod._device is not None and mod._device != dev):
+        raise ValueError("cu_seqlens and the modifier's arrays must be on %s" % dev)
+    for name, n, want in zip(("alibi_slopes", "prefix_len", "row_start"), mod._sizes, (desc.hq, desc.nseq, T)):
+        if n is not None and n != want:
+            raise ValueError("%s must have %d elements, not %d" % (name, want, n))
+    return dev
+
+
+def lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, ws=None, stream=None):
+    dev = _check_attention(desc, mod, q, k, v, [
+        ("o", o, desc.hq), ("lse", lse, (torch.float32, desc.hq * desc.total_tokens))])
+    L = _load()
+    args = [t.data_ptr() for t in (q, k, v, o, lse)] + [_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()]
+    _check(_on_device(dev, lambda s: L.lf_attn_fwd_mod(ctypes.byref(desc), ctypes.byref(mod), *args, s), stream),
+           "lf_attn_fwd_mod")
+
+
+def lf_attn_bwd_mod(desc, mod, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv,
+                    ws, stream=None):
+    rows = (torch.float32, desc.hq * desc.total_tokens)
+    heads = desc.nseq * desc.hq
+    nb = heads * ((desc.max_seqlen + desc.block_q - 1) // desc.block_q)
+    dev = _check_attention(desc, mod, q, k, v, [
+        ("o", o, desc.hq), ("lse", lse, rows), ("dout", dout, desc.hq), ("D", D, rows),
+        ("block_weight", block_weight, (torch.float32, nb)), ("kept_idx", kept_idx, (torch.int32, nb)),
+        ("kept_cnt", kept_cnt, (torch.int32, heads)), ("dq", dq, desc.hq), ("dk", dk, desc.hkv),
+        ("dv", dv, desc.hkv)])
+    L = _load()
+    args = [None if t is None else t.data_ptr()
+            for t in (q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv, ws)]
+    args.append(0 if ws is None else ws.numel() * ws.element_size())
+    _check(_on_device(dev, lambda s: L.lf_attn_bwd_mod(ctypes.byref(desc), ctypes.byref(mod), *args, s), stream),
+           "lf_attn_bwd_mod")
+
+
+def shared_prompt_tables(prompt_lens, answer_lens, device="cuda"):
+    """Tables of a batch in which many answers share one prompt.  Segment s is packed as its
+    prompt (prompt_lens[s] tokens) followed by its answers (answer_lens[s], a list of
+    lengths).  Returns (cu_seqlens, prefix_len, row_start, positions), int32: the mask's
+    arrays for make_score_mod(prefix_len=..., prefix_causal=True, row_start=...), and each
+    token's position, every answer's continuing its prompt's, for qk_norm_rope."""
+    cu, start, pos = [0], [], []
+    for p, answers in zip(prompt_lens, answer_lens, strict=True):
+        at = int(p)
+        start.append(torch.zeros(at, dtype=torch.int32))
+        pos.append(torch.arange(at, dtype=torch.int32))
+        for n in answers:
+            start.append(torch.full((int(n),), at, dtype=torch.int32))
+            pos.append(torch.arange(int(p), int(p) + int(n), dtype=torch.int32))
+            at += int(n)
+        cu.append(cu[-1] + at)
+    tables = (torch.tensor(cu, dtype=torch.int32), torch.tensor(list(prompt_lens), dtype=torch.int32),
+              torch.cat(start), torch.cat(pos))
+    return tuple(t.to(device) for t in tables)
+
+
+# --------------------------------------------------------------------------------------
+# norms of the query and key heads with the position rotation
+# --------------------------------------------------------------------------------------
 def rope_cos_sin(npos: int, rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
     """Table of lf_qk_norm_rope: fp32 [npos, rot], row p the cosines, then the sines, of
     p * theta^(-2i/rot), i < rot/2.  The angles are computed in 64 bits, so that far

@@ -19,8 +19,9 @@ import math
 
 import torch
 
-from . import (Buffers, lf_attn_bwd, lf_attn_fwd, lf_block_select, lf_qk_norm_rope,
-               lf_qk_norm_rope_bwd, lf_qk_workspace_size, make_desc, make_qk_desc)
+from . import (Buffers, lf_attn_bwd, lf_attn_bwd_mod, lf_attn_fwd, lf_attn_fwd_mod, lf_block_select,
+               lf_qk_norm_rope, lf_qk_norm_rope_bwd, lf_qk_workspace_size, make_desc, make_qk_desc,
+               make_score_mod)
 
 _step_counter = itertools.count()
 
@@ -28,7 +29,7 @@ _step_counter = itertools.count()
 class LazyFlashAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal, block_q,
-                softmax_scale, selection_out):
+                softmax_scale, selection_out, mod):
         for t in (q, k, v):
             if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("q, k, v must be contiguous bf16 CUDA tensors")
@@ -38,7 +39,11 @@ class LazyFlashAttention(torch.autograd.Function):
         desc = make_desc(cu_seqlens, max_seqlen, T, hq, hkv, d, scale, causal, block_q)
         o = torch.empty_like(q)
         lse = torch.empty(hq, T, dtype=torch.float32, device=q.device)
-        lf_attn_fwd(desc, q, k, v, o, lse)
+        if mod is None:
+            lf_attn_fwd(desc, q, k, v, o, lse)
+        else:
+            lf_attn_fwd_mod(desc, mod, q, k, v, o, lse)
+        ctx.mod = mod
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
         ctx.desc = desc
         ctx.delta = float(delta)
@@ -56,25 +61,39 @@ class LazyFlashAttention(torch.autograd.Function):
         bufs = Buffers(desc, device=q.device, forward=False)
         lf_block_select(desc, dout, o, ctx.delta, ctx.seed, ctx.step, 0, bufs.norm, bufs.D,
                         bufs.tau, bufs.w, bufs.keep, bufs.kept_idx, bufs.kept_cnt)
-        lf_attn_bwd(desc, q, k, v, o, lse, dout, bufs.D, bufs.w, bufs.kept_idx, bufs.kept_cnt,
-                    bufs.dq, bufs.dk, bufs.dv, bufs.ws)
+        args = (q, k, v, o, lse, dout, bufs.D, bufs.w, bufs.kept_idx, bufs.kept_cnt, bufs.dq, bufs.dk,
+                bufs.dv, bufs.ws)
+        if ctx.mod is None:
+            lf_attn_bwd(desc, *args)
+        else:
+            lf_attn_bwd_mod(desc, ctx.mod, *args)
         if ctx.selection_out is not None:
             ctx.selection_out.update(norm=bufs.norm, tau=bufs.tau, keep=bufs.keep,
                                      weight=bufs.w, kept_cnt=bufs.kept_cnt, step=ctx.step)
-        return bufs.dq, bufs.dk, bufs.dv, None, None, None, None, None, None, None, None, None
+        return (bufs.dq, bufs.dk, bufs.dv) + (None,) * 10
 
 
 def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step=None,
-                        causal=True, block_q=128, softmax_scale=None, selection_out=None):
+                        causal=True, block_q=128, softmax_scale=None, selection_out=None,
+                        softcap=0.0, alibi_slopes=None, prefix_len=None, prefix_causal=False,
+                        row_start=None):
     """Dense attention forward, LazyFlash block-sparse backward.
 
     ``step`` defaults to a process-wide counter, so every backward draws a
     fresh mask; pass it explicitly to replay a draw.  If ``selection_out`` is a
     dict, the backward stores in it the selection it drew: block norms ``norm``,
     thresholds ``tau``, ``keep``, block weights ``weight`` ([nseq, hq, nbmax]
-    device tensors), ``kept_cnt`` and the Philox ``step`` used."""
+    device tensors), ``kept_cnt`` and the Philox ``step`` used.
+
+    ``softcap`` (scores capped by a tanh), ``alibi_slopes`` [hq] (a bias that falls with the
+    distance; no gradient), ``prefix_len`` [nseq], ``prefix_causal`` and ``row_start`` [T]
+    (prefix, document, window and shared-prompt masks) modify the scores of both directions:
+    lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's."""
+    mod = None
+    if softcap or alibi_slopes is not None or prefix_len is not None or row_start is not None or prefix_causal:
+        mod = make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
-                                    block_q, softmax_scale, selection_out)
+                                    block_q, softmax_scale, selection_out, mod)
 
 
 class QkNormRope(torch.autograd.Function):

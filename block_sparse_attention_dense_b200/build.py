@@ -10,13 +10,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblazyflash.so")
 SOURCES = ["lazyflash.cu"]
-HEADERS = ["lf_device.cuh", "lf_select.cuh", "lf_fwd.cuh", "lf_bwd.cuh", "lf_qknorm.cuh"]
+HEADERS = ["lf_device.cuh", "lf_select.cuh", "lf_fwd.cuh", "lf_bwd.cuh", "lf_mod.cuh", "lf_qknorm.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared",
     "--diag-suppress", "177",
+    "--split-compile=0",   # the kernel variants compile side by side
 ]
 
 

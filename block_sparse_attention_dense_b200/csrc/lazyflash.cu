@@ -80,6 +80,11 @@ BwdWs bwd_ws_layout(const lf_attn_desc* d, bool need_D) {
     return w;
 }
 size_t bwd_ws_bytes(const lf_attn_desc* d, bool need_D) { return bwd_ws_layout(d, need_D).total; }
+// ... then, for modified scores with row_start, a row index per key
+size_t key_last_offset(const lf_attn_desc* d) { return bwd_ws_bytes(d, true); }
+size_t bwd_ws_bytes_mod(const lf_attn_desc* d) {
+    return key_last_offset(d) + al256((size_t)d->total_tokens * sizeof(int32_t));
+}
 
 // [T][H][d] bf16 -> 3-D map (d, H, T), 64 x 1 x `rows` boxes, 128-byte swizzle.
 bool make_thd_map(CUtensorMap* m, const void* base, int T, int H, int D, int rows = 128) {
@@ -114,9 +119,45 @@ inline lf_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? LF_OK : LF_ERR_CUDA;
 }
 
-template <int D>
-lf_status launch_fwd(const lf_attn_desc* d, const void* q, const void* k, const void* v, void* o,
-                     float* lse, cudaStream_t st) {
+lf_status check_mod(const lf_attn_desc* d, const lf_score_mod* m) {
+    if (!m) return LF_ERR_INVALID_ARG;
+    if (m->softcap != 0.f && !(m->softcap >= 1e-3f && m->softcap <= 1e6f)) return LF_ERR_INVALID_ARG;
+    // read value by value: slices of longer arrays are fine
+    for (const void* p : {static_cast<const void*>(m->alibi_slopes), static_cast<const void*>(m->prefix_len),
+                          static_cast<const void*>(m->row_start)})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return LF_ERR_INVALID_ARG;
+    if (m->prefix_causal != 0 && m->prefix_causal != 1) return LF_ERR_INVALID_ARG;
+    if (m->prefix_causal && !m->prefix_len) return LF_ERR_INVALID_ARG;
+    // the masks say which keys a causal row sees besides, or no longer
+    if ((m->prefix_len || m->row_start) && !d->causal) return LF_ERR_UNSUPPORTED;
+    return LF_OK;
+}
+
+// The kernels' variant for a modifier, and its parameters.
+int mod_variant(const lf_score_mod* m) {
+    return !m ? 0 : (m->softcap != 0.f ? lf::kModCap : 0) | (m->alibi_slopes ? lf::kModBias : 0) |
+                        (m->prefix_len || m->row_start ? lf::kModMask : 0);
+}
+lf::ModParams mod_params(const lf_attn_desc* d, const lf_score_mod* m) {
+    lf::ModParams p{};
+    if (!m) return p;
+    if (m->softcap != 0.f) {
+        const double c = m->softcap * 1.4426950408889634;
+        p.cap_in = static_cast<float>((double)d->softmax_scale / m->softcap);
+        p.cap_out = static_cast<float>(c);
+        p.cap_out_inv = static_cast<float>(1.0 / c);
+        for (int i = 0; i < lf::kCapTerms; ++i) p.cap_coef[i] = static_cast<float>(c * lf::kCapCoef[i]);
+    }
+    p.slopes = m->alibi_slopes;
+    p.prefix = m->prefix_len;
+    p.prefix_causal = m->prefix_causal;
+    p.row_start = m->row_start;
+    return p;
+}
+
+template <int D, int kMod>
+lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void* q, const void* k,
+                     const void* v, void* o, float* lse, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     if (!make_thd_map(&mq, q, d->total_tokens, d->hq, D) ||
         !make_thd_map(&mk, k, d->total_tokens, d->hkv, D) ||
@@ -133,8 +174,9 @@ lf_status launch_fwd(const lf_attn_desc* d, const void* q, const void* k, const 
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
+    p.mod = mod_params(d, mod);
     const uint32_t smem = lf::FwdSmem<D>::kAlloc;
-    if (cudaFuncSetAttribute(lf::attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(lf::attn_fwd_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
         return LF_ERR_CUDA;
     // The kernel's warpgroups resize their register budgets (setmaxnreg); the larger
@@ -142,7 +184,7 @@ lf_status launch_fwd(const lf_attn_desc* d, const void* q, const void* k, const 
     // build that launches with fewer than the budgets add up to must not run (its
     // softmax warps would wait for registers that never come).
     cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, lf::attn_fwd_kernel<D>) != cudaSuccess) return LF_ERR_CUDA;
+    if (cudaFuncGetAttributes(&fa, lf::attn_fwd_kernel<D, kMod>) != cudaSuccess) return LF_ERR_CUDA;
     const int launch_regs = (fa.numRegs + 7) / 8 * 8;
     if (launch_regs * lf::kFwdThreads < 128 * lf::kFwdCtrlRegs + 256 * lf::kFwdSoftmaxRegs)
         return LF_ERR_UNSUPPORTED;
@@ -159,7 +201,7 @@ lf_status launch_fwd(const lf_attn_desc* d, const void* q, const void* k, const 
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return LF_ERR_CUDA;
     p.tile_major = (long long)grid.x * grid.y <= 8LL * nsm ? 1 : 0;
-    lf::attn_fwd_kernel<D><<<grid, lf::kFwdThreads, smem, st>>>(mq, mk, mv, p);
+    lf::attn_fwd_kernel<D, kMod><<<grid, lf::kFwdThreads, smem, st>>>(mq, mk, mv, p);
     return launch_status();
 }
 
@@ -176,9 +218,10 @@ lf_status launch_norms(const lf_attn_desc* d, const void* dout, const void* o, f
 
 // The backward: prologue over kept blocks (dQ accumulator rows zeroed; D computed into
 // the workspace when the caller passed none), attn_bwd_kernel, dQ conversion.
-template <int D>
-lf_status launch_bwd(const lf_attn_desc* d, const void* q, const void* k, const void* v,
-                     const void* o, const float* lse, const void* dout, const float* Dgiven,
+// key_last: scratch of a modifier with row_start.
+template <int D, int kMod>
+lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* q,
+                     const void* k, const void* v, const void* o, const float* lse, const void* dout, const float* Dgiven,
                      const float* w, const int32_t* kidx, const int32_t* kcnt, void* dq, void* dk,
                      void* dv, void* ws, cudaStream_t st) {
     // Q and dO also in 64-row boxes: a query tile with one live half loads only that half
@@ -222,7 +265,8 @@ lf_status launch_bwd(const lf_attn_desc* d, const void* q, const void* k, const 
     float* Dw = Dgiven ? nullptr : reinterpret_cast<float*>(base + bwd_ws_layout(d, true).D);
     lf::bwd_prologue_kernel<D><<<blocks, lf::kNormThreads, 0, st>>>(
         d->cu_seqlens, d->total_tokens, d->max_seqlen, d->hq, d->block_q, nbmax_of(d), w, dq_acc,
-        static_cast<const __nv_bfloat16*>(dout), static_cast<const __nv_bfloat16*>(o), Dw);
+        static_cast<const __nv_bfloat16*>(dout), static_cast<const __nv_bfloat16*>(o), Dw,
+        mod ? mod->row_start : nullptr, key_last);
     if (launch_status() != LF_OK) return LF_ERR_CUDA;
     const float* Dv = Dgiven ? Dgiven : Dw;
     lf::BwdParams p{};
@@ -246,9 +290,11 @@ lf_status launch_bwd(const lf_attn_desc* d, const void* q, const void* k, const 
     p.kept_idx = kidx;
     p.kept_cnt = kcnt;
     p.dq_acc = dq_acc;
+    p.mod = mod_params(d, mod);
+    p.key_last = key_last;
     const uint32_t smem = lf::BwdSmem<D>::kAlloc;
     // 64-row selection blocks: the variant that skips a tile's dropped half
-    auto kern = d->block_q == 64 ? lf::attn_bwd_kernel<D, true> : lf::attn_bwd_kernel<D, false>;
+    auto kern = d->block_q == 64 ? lf::attn_bwd_kernel<D, true, kMod> : lf::attn_bwd_kernel<D, false, kMod>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LF_ERR_CUDA;
     dim3 grid(ntiles_of(d), d->hq / p.heads_per_cta, d->nseq);
@@ -275,6 +321,39 @@ lf_status launch_bwd(const lf_attn_desc* d, const void* q, const void* k, const 
                                                    static_cast<uint4*>(dv), nkv8, 1.0f);
     }
     return launch_status();
+}
+
+// f(head dim, variant of the modified scores) as compile-time constants.
+template <typename F>
+lf_status by_variant(const lf_attn_desc* d, const lf_score_mod* mod, F&& f) {
+    auto by_d = [&](auto v) {
+        return d->d == 128 ? f(std::integral_constant<int, 128>{}, v) : f(std::integral_constant<int, 64>{}, v);
+    };
+    switch (mod_variant(mod)) {
+        case 0: return by_d(std::integral_constant<int, 0>{});
+        case 1: return by_d(std::integral_constant<int, 1>{});
+        case 2: return by_d(std::integral_constant<int, 2>{});
+        case 3: return by_d(std::integral_constant<int, 3>{});
+        case 4: return by_d(std::integral_constant<int, 4>{});
+        case 5: return by_d(std::integral_constant<int, 5>{});
+        case 6: return by_d(std::integral_constant<int, 6>{});
+        default: return by_d(std::integral_constant<int, 7>{});
+    }
+}
+lf_status launch_fwd_any(const lf_attn_desc* d, const lf_score_mod* mod, const void* q, const void* k,
+                         const void* v, void* o, float* lse, cudaStream_t st) {
+    return by_variant(d, mod, [&](auto D, auto M) {
+        return launch_fwd<decltype(D)::value, decltype(M)::value>(d, mod, q, k, v, o, lse, st);
+    });
+}
+lf_status launch_bwd_any(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* q,
+                         const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                         const float* Dgiven, const float* w, const int32_t* kidx, const int32_t* kcnt, void* dq,
+                         void* dk, void* dv, void* ws, cudaStream_t st) {
+    return by_variant(d, mod, [&](auto D, auto M) {
+        return launch_bwd<decltype(D)::value, decltype(M)::value>(d, mod, key_last, q, k, v, o, lse, dout, Dgiven,
+                                                                  w, kidx, kcnt, dq, dk, dv, ws, st);
+    });
 }
 
 lf_status check_qk_desc(const lf_qk_desc* d) {
@@ -488,15 +567,13 @@ lf_status lf_workspace_size(const lf_attn_desc* desc, int which, size_t* bytes) 
     switch (which) {
         case LF_WS_FWD: *bytes = 0; return LF_OK;
         case LF_WS_SELECT: *bytes = 0; return LF_OK;
-        case LF_WS_BWD: *bytes = bwd_ws_bytes(desc, true); return LF_OK;
+        case LF_WS_BWD: *bytes = bwd_ws_bytes_mod(desc); return LF_OK;
     }
     return LF_ERR_INVALID_ARG;
 }
 
-lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,
-                      void* o, float* lse, void* ws, size_t ws_bytes, lf_stream_t stream) {
-    (void)ws;
-    (void)ws_bytes;
+static lf_status attn_fwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                               const void* k, const void* v, void* o, float* lse, lf_stream_t stream) {
     lf_status st = check_desc(desc);
     if (st != LF_OK) return st;
     if (!q || !k || !v || !o || !lse) return LF_ERR_INVALID_ARG;
@@ -506,8 +583,24 @@ lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, co
     if (desc->total_tokens == 0 || desc->max_seqlen == 0) return LF_OK;
     if ((st = prepare_device()) != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return mirror_after(desc->d == 128 ? launch_fwd<128>(desc, q, k, v, o, lse, s)
-                                       : launch_fwd<64>(desc, q, k, v, o, lse, s), s);
+    return mirror_after(launch_fwd_any(desc, mod, q, k, v, o, lse, s), s);
+}
+
+lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,
+                      void* o, float* lse, void* ws, size_t ws_bytes, lf_stream_t stream) {
+    (void)ws;
+    (void)ws_bytes;
+    return attn_fwd_impl(desc, nullptr, q, k, v, o, lse, stream);
+}
+
+lf_status lf_attn_fwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                          const void* k, const void* v, void* o, float* lse, void* ws,
+                          size_t ws_bytes, lf_stream_t stream) {
+    (void)ws;
+    (void)ws_bytes;
+    lf_status st = check_desc(desc);
+    if (st == LF_OK) st = check_mod(desc, mod);
+    return st != LF_OK ? st : attn_fwd_impl(desc, mod, q, k, v, o, lse, stream);
 }
 
 static lf_status block_select_impl(const lf_attn_desc* desc, const void* dout, const void* o,
@@ -581,11 +674,11 @@ lf_status lf_block_select_rule(const lf_attn_desc* desc, const void* dout, const
                              block_weight, keep, kept_idx, kept_cnt, stream);
 }
 
-lf_status lf_attn_bwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,
-                      const void* o, const float* lse, const void* dout, const float* D,
-                      const float* block_weight, const int32_t* kept_idx,
-                      const int32_t* kept_cnt, void* dq, void* dk, void* dv, void* ws,
-                      size_t ws_bytes, lf_stream_t stream) {
+static lf_status attn_bwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                               const void* k, const void* v, const void* o, const float* lse,
+                               const void* dout, const float* D, const float* block_weight,
+                               const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
+                               void* dv, void* ws, size_t ws_bytes, lf_stream_t stream) {
     lf_status st = check_desc(desc);
     if (st != LF_OK) return st;
     if (!q || !k || !v || !lse || !dout || !block_weight || !kept_idx || !kept_cnt || !dq ||
@@ -598,14 +691,37 @@ lf_status lf_attn_bwd(const lf_attn_desc* desc, const void* q, const void* k, co
     if ((o && !aligned16(o)) || (D && !aligned16(D))) return LF_ERR_INVALID_ARG;
     if ((st = pending_device_error()) != LF_OK) return st;
     if (desc->total_tokens == 0 || desc->max_seqlen == 0) return LF_OK;
-    if (!ws || ws_bytes < bwd_ws_bytes(desc, D == nullptr)) return LF_ERR_WORKSPACE;
+    const bool starts = mod && mod->row_start;
+    if (!ws || ws_bytes < (starts ? bwd_ws_bytes_mod(desc) : bwd_ws_bytes(desc, D == nullptr)))
+        return LF_ERR_WORKSPACE;
+    int32_t* key_last =
+        starts ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + key_last_offset(desc)) : nullptr;
     if ((st = prepare_device()) != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return mirror_after(desc->d == 128 ? launch_bwd<128>(desc, q, k, v, o, lse, dout, D, block_weight,
-                                                         kept_idx, kept_cnt, dq, dk, dv, ws, s)
-                                       : launch_bwd<64>(desc, q, k, v, o, lse, dout, D, block_weight,
-                                                        kept_idx, kept_cnt, dq, dk, dv, ws, s),
+    return mirror_after(launch_bwd_any(desc, mod, key_last, q, k, v, o, lse, dout, D, block_weight, kept_idx,
+                                       kept_cnt, dq, dk, dv, ws, s),
                         s);
+}
+
+lf_status lf_attn_bwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,
+                      const void* o, const float* lse, const void* dout, const float* D,
+                      const float* block_weight, const int32_t* kept_idx,
+                      const int32_t* kept_cnt, void* dq, void* dk, void* dv, void* ws,
+                      size_t ws_bytes, lf_stream_t stream) {
+    return attn_bwd_impl(desc, nullptr, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv,
+                         ws, ws_bytes, stream);
+}
+
+lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                          const void* k, const void* v, const void* o, const float* lse,
+                          const void* dout, const float* D, const float* block_weight,
+                          const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
+                          void* dv, void* ws, size_t ws_bytes, lf_stream_t stream) {
+    lf_status st = check_desc(desc);
+    if (st == LF_OK) st = check_mod(desc, mod);
+    return st != LF_OK ? st
+                       : attn_bwd_impl(desc, mod, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq,
+                                       dk, dv, ws, ws_bytes, stream);
 }
 
 lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const void* k,
@@ -633,10 +749,8 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
     if (st != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // launch_bwd clears the accumulators it uses before the kernel
-    return mirror_after(desc->d == 128 ? launch_bwd<128>(desc, q, k, v, o, lse, dout, D, block_weight,
-                                                         kept_idx, kept_cnt, dq, dk, dv, ws, s)
-                                       : launch_bwd<64>(desc, q, k, v, o, lse, dout, D, block_weight,
-                                                        kept_idx, kept_cnt, dq, dk, dv, ws, s),
+    return mirror_after(launch_bwd_any(desc, nullptr, nullptr, q, k, v, o, lse, dout, D, block_weight, kept_idx,
+                                       kept_cnt, dq, dk, dv, ws, s),
                         s);
 }
 

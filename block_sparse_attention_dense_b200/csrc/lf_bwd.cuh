@@ -39,6 +39,12 @@
 // same block's weight, and the kernel keeps one phase per pair (the skipping
 // variant's bookkeeping cost about 4 % there, A/B on one GPU).
 //
+// kMod selects modified scores (lf_mod.cuh) at compile time.  P is recomputed from the
+// capped and biased score, dS takes the cap's derivative 1 - tanh^2, and under a mask the
+// CTA visits only the kept query tiles between the first row that may see its keys and the
+// last one that does; within them, the rows that see a key are one run, so that a thread
+// (one key) compares the query's index with two bounds.
+//
 // Tensor memory (512 columns): dV [0,128) dK [128,256); half 0: S^T [256,320)
 // (after the element-wise pass: P^T in its first 32 columns, dS^T in the next 32,
 // both bf16 packed two per column), dP^T then dQ^T [320,384); half 1: [384,448),
@@ -47,6 +53,7 @@
 #pragma once
 
 #include "lf_device.cuh"
+#include "lf_mod.cuh"
 
 namespace lf {
 
@@ -72,6 +79,8 @@ struct BwdParams {
     int tile_major;
     __nv_bfloat16* dk_out;
     __nv_bfloat16* dv_out;
+    ModParams mod;             // read where kMod is not 0
+    const int32_t* key_last;   // [T] last row of the segment that sees the key, with mod.row_start
 };
 
 constexpr uint32_t kAccBox = 128 * 32 * 4;   // one staged 32-column fp32 box of a KV tile
@@ -89,7 +98,8 @@ struct BwdSmem {
     static constexpr uint32_t kVec = kDS + 2 * kHalfDS;        // lse*log2e [128], D [128]
     static constexpr uint32_t kBars = kVec + 2 * 128 * 4;
     static constexpr uint32_t kHeads = kBars + 256;            // int2 per query head of the CTA
-    static constexpr uint32_t kBytes = kHeads + kMaxHeadsPerCta * 8;
+    static constexpr uint32_t kSlopes = kHeads + kMaxHeadsPerCta * 8;   // float per query head
+    static constexpr uint32_t kBytes = kSlopes + kMaxHeadsPerCta * 4;
     static constexpr uint32_t kAlloc = kBytes + 1024;
 };
 
@@ -124,19 +134,22 @@ __device__ __forceinline__ int lower_bound_warp(const int32_t* list, int cnt, in
 }
 
 // Before the walk, the warps of the CTA find, head by head (warp w takes heads w,
-// w + 16, ...), each head's first kept block at or after the CTA's first query tile
-// with the warp-parallel search, and store (position, count) in shared memory; the
+// w + 16, ...), each head's first kept block at or after the CTA's first query row
+// with the warp-parallel search, and store (position, end) in shared memory; the
 // return value says whether that head has any tile to visit (the same on every lane).
-__device__ __forceinline__ bool find_head_starts(const BwdParams& p, int G, int g, int s, int jt,
-                                                 int len, int2* heads) {
+// kMask: the walk also ends after the block of row last_row.
+template <bool kMask>
+__device__ __forceinline__ bool find_head_starts(const BwdParams& p, int G, int g, int s, int first_row,
+                                                 int last_row, int len, int2* heads) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first_block = p.causal ? (jt * 128) / p.block_q : 0;
+    const int first_block = first_row / p.block_q;
     const int nb = (len + p.block_q - 1) / p.block_q;
     bool any = false;
     for (int hh = warp; hh < G; hh += kBwdThreads / 32) {
         const int h = g * G + hh;
         const int32_t* l = p.kept_idx + ((size_t)s * p.hq + h) * p.nbmax;
-        const int c = min(max(p.kept_cnt[(size_t)s * p.hq + h], 0), p.nbmax);
+        int c = min(max(p.kept_cnt[(size_t)s * p.hq + h], 0), p.nbmax);
+        if (kMask && last_row + 1 < len) c = lower_bound_warp(l, c, last_row / p.block_q + 1);
         const int start = first_block == 0 ? 0 : lower_bound_warp(l, c, first_block);
         if (lane == 0) heads[hh] = make_int2(start, c);
         if (start < c) {
@@ -207,7 +220,7 @@ __device__ __forceinline__ float half_weight(const BwdParams& p, int s, int h, i
     return p.block_weight[((size_t)s * p.hq + h) * p.nbmax + q0 / p.block_q];
 }
 
-template <int D, bool kHalves>
+template <int D, bool kHalves, int kMod>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -215,6 +228,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_do64,
                     BwdParams prm) {
     using L = BwdSmem<D>;
+    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
     static_assert(2 * (D / 32) * kAccBox <= 4 * L::kTile, "dK/dV staging must fit the Q/dO buffers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -288,7 +302,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     // every head's first kept tile for this KV tile; does the tile have any work?
     int2* head_starts = reinterpret_cast<int2*>(smem + L::kHeads);
-    const bool has = find_head_starts(prm, prm.heads_per_cta, hgrp, s, jt, len, head_starts);
+    // the rows that may see the tile's keys: from first_row (0 for a prefix seen whole) to last_row
+    int first_row = prm.causal ? jt * 128 : 0, last_row = len - 1, P = 0;
+    if constexpr (kMask) {
+        bool bad = false;
+        P = prefix_of(prm.mod, s, len, bad);
+        if (bad && tid == 0) report_error(18, kErrBadMask);
+        const bool in_prefix = jt * 128 < P;
+        if (in_prefix && !prm.mod.prefix_causal) first_row = 0;
+        if (!in_prefix && prm.mod.row_start) last_row = prm.key_last[seg0 + min(jt * 128 + 127, len - 1)];
+    }
+    const bool has = find_head_starts<kMask>(prm, prm.heads_per_cta, hgrp, s, first_row, last_row, len, head_starts);
+    float* slopes_s = reinterpret_cast<float*>(smem + L::kSlopes);   // -slope log2(e) per query head
+    if constexpr (kBias) {
+        if (tid < prm.heads_per_cta)
+            slopes_s[tid] = prm.mod.slopes[hgrp * prm.heads_per_cta + tid] * -1.4426950408889634f;
+    }
     tc_fence_before();
     const bool any = __syncthreads_or(has) != 0;   // the same answer in every role
     tc_fence_after();
@@ -523,7 +552,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // P = 0 where kv_cmp > the query's index: the key follows the query (causal), or
         // the KV row lies past the segment's end (its key belongs to the next segment, so
         // its exponent is not bounded by this query's LSE and must not reach the products)
-        const int kv_cmp = !kv_valid ? 0x7fffffff : (prm.causal ? kv_local : (int)0x80000000);
+        int kv_cmp = !kv_valid ? 0x7fffffff : (prm.causal ? kv_local : (int)0x80000000);
+        int q_last = 0x7fffffff;   // kMask: P = 0 past this query index as well
+        if constexpr (kMask) {
+            if (kv_valid && kv_local < P) {
+                if (!prm.mod.prefix_causal) kv_cmp = (int)0x80000000;
+            } else if (kv_valid && prm.mod.row_start) {
+                q_last = prm.key_last[seg0 + kv_local];
+            }
+        }
         int n = 0;
         // parity of each half's live pairs processed (bit hf: the half's barrier phase);
         // bits of one register rather than an array indexed by the half loop, which would
@@ -591,8 +628,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 // fp32 columns of the other)
                 named_bar_sync(3, 256);
                 if (!ok) { failed = true; continue; }
+                // distances |t - u|: column minus key, exact in fp32 (below 2^24)
+                const float dist0 = kBias ? static_cast<float>(q0 + hf * 64 - kv_local) : 0.f;
+                const float slope = kBias ? slopes_s[e.h - hgrp * prm.heads_per_cta] : 0.f;
                 auto chunk = [&](int c, const uint32_t (&sr)[16], const uint32_t (&dr)[16]) {
                     uint32_t pk[8], dk_[8];
+                    const float dist_c = dist0 + static_cast<float>(c * 16);
+                    bool far = false;   // a capped score of the warp lies outside the fit's range
+                    if constexpr (kCap) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2)
+                            top = fmax3(top, fabsf(__uint_as_float(sr[i])), fabsf(__uint_as_float(sr[i + 1])));
+                        far = __any_sync(0xffffffffu, !(top * prm.mod.cap_in <= kCapRange));
+                    }
 #pragma unroll
                     for (int e4 = 0; e4 < 4; ++e4) {
                         const int col0 = hf * 64 + c * 16 + 4 * e4;
@@ -610,12 +659,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                                           __uint_as_float(sr[4 * e4 + u + 1]));
                             const float2 dp2 = make_float2(__uint_as_float(dr[4 * e4 + u]),
                                                            __uint_as_float(dr[4 * e4 + u + 1]));
-                            const float2 x = f2_fma(s2, sc2, nl);
+                            float2 x, damp = make_float2(1.f, 1.f);
+                            if constexpr (kCap) {
+                                const float2 y = far ? cap_any(prm.mod, s2) : cap_near(prm.mod, s2);
+                                const float2 th = f2_mul(y, make_float2(prm.mod.cap_out_inv, prm.mod.cap_out_inv));
+                                damp = f2_fma(th, make_float2(-th.x, -th.y), damp);   // 1 - tanh^2
+                                x = f2_add(y, nl);
+                            } else {
+                                x = f2_fma(s2, sc2, nl);
+                            }
+                            if constexpr (kBias) {
+                                const float2 dist = f2_add(make_float2(dist_c, dist_c), make_float2(4 * e4 + u, 4 * e4 + u + 1));
+                                x = f2_fma(make_float2(fabsf(dist.x), fabsf(dist.y)), make_float2(slope, slope), x);
+                            }
                             float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                            if (kv_cmp > q0 + col0 + u) p0 = 0.f;
-                            if (kv_cmp > q0 + col0 + u + 1) p1 = 0.f;
+                            if (kv_cmp > q0 + col0 + u || (kMask && q_last < q0 + col0 + u)) p0 = 0.f;
+                            if (kv_cmp > q0 + col0 + u + 1 || (kMask && q_last < q0 + col0 + u + 1)) p1 = 0.f;
                             const float2 pw2 = f2_mul(make_float2(p0, p1), w2);
-                            const float2 ds2 = f2_mul(pw2, f2_sub(dp2, dv2));
+                            float2 ds2 = f2_mul(pw2, f2_sub(dp2, dv2));
+                            if constexpr (kCap) ds2 = f2_mul(ds2, damp);
                             pw[u] = pw2.x;
                             pw[u + 1] = pw2.y;
                             dsw[u] = ds2.x;

@@ -22,11 +22,19 @@
 // Tensor memory (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d),
 // O1 [384,384+d); P_t (bf16, packed two per column) over S_t [0,64).  Reuse
 // of a region by a later MMA relies on tcgen05.mma executing in issue order.
+//
+// kMod selects modified scores (lf_mod.cuh) at compile time: the tanh cap and the distance
+// bias in the softmax warps, before the row maximum; the masks also in the KV tiles that
+// are visited.  Under a mask the two query tiles of a CTA share one list of KV tiles (the
+// prefix's, then a run up to the diagonal), and a tile that has nothing in a step only
+// hands the step's stages back, so that a document's end between the two does not make the
+// later one walk the earlier one's keys.
 #pragma once
 
 #include <climits>
 
 #include "lf_device.cuh"
+#include "lf_mod.cuh"
 
 namespace lf {
 
@@ -37,6 +45,7 @@ struct FwdParams {
     int tile_major;            // CTA order: 1 = KV head fastest (see the kernel)
     __nv_bfloat16* o;
     float* lse;
+    ModParams mod;             // read where kMod is not 0
 };
 
 template <int D>
@@ -57,11 +66,12 @@ constexpr int kFwdCtrlRegs = 64;
 constexpr int kFwdSoftmaxRegs = 216;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a rescale
 
-template <int D>
+template <int D, int kMod>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, FwdParams prm) {
     using L = FwdSmem<D>;
+    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -107,10 +117,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int m = npairs - 1 - (pg - first_unit_of_segment(seg0, s, 8));   // longest rows first
     if (m < 0) return;
     const bool two = 2 * m + 1 < ntiles;                     // tile 1 exists
-    // KV tiles each query tile needs
-    const int nkv0 = prm.causal ? 2 * m + 1 : ntiles;
-    const int nkv1 = two ? (prm.causal ? 2 * m + 2 : ntiles) : 0;
+    // KV tiles each query tile needs (under a mask: its steps up to the last one with work)
+    int nkv0 = prm.causal ? 2 * m + 1 : ntiles;
+    int nkv1 = two ? (prm.causal ? 2 * m + 2 : ntiles) : 0;
+    int P = 0;                       // prefix length
+    PairSteps steps{};
+    TileRuns runs0{}, runs1{};
+    if constexpr (kMask) {
+        bool bad = false;
+        P = prefix_of(prm.mod, s, len, bad);
+        if (bad && threadIdx.x == 0) report_error(17, kErrBadMask);
+        runs0 = tile_runs(prm.mod, 2 * m, seg0, len, P);
+        runs1 = two ? tile_runs(prm.mod, 2 * m + 1, seg0, len, P) : TileRuns{0, 0, 0};
+        steps.n_prefix = max(runs0.np, runs1.np);
+        steps.lo = max(runs0.lo, steps.n_prefix);
+        nkv0 = runs0.steps(steps);
+        nkv1 = two ? runs1.steps(steps) : 0;
+    }
     const int nkv = nkv0 > nkv1 ? nkv0 : nkv1;
+    // the KV tile of step i, and whether query tile t has work there
+    auto kv_tile = [&](int i) { return kMask ? steps.tile(i) : i; };
+    auto has_work = [&](int t, int i) {
+        if constexpr (kMask) return t ? runs1.has(steps.tile(i)) : runs0.has(steps.tile(i));
+        return true;
+    };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t s_base = smem_addr(smem);
@@ -166,14 +196,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mbar_arrive_expect_tx(&bar_k_full[st], L::kTile);
                     for (int c = 0; c < L::kPanels; ++c)
                         tma_load_3d(smem + L::kK + st * L::kTile + c * kPanelBytes, &tm_k, &bar_k_full[st],
-                                    c * 64, g, seg0 + j * 128);
+                                    c * 64, g, seg0 + kv_tile(j) * 128);
                     kpar[st] = (j >> 1) & 1;
                     ++kfill;
                     if (j >= 2 && !mbar_wait_or_abort(&bar_v_empty[st], ((j >> 1) - 1) & 1, 22, abort_flag)) break;
                     mbar_arrive_expect_tx(&bar_v_full[st], L::kTile);
                     for (int c = 0; c < L::kPanels; ++c)
                         tma_load_3d(smem + L::kV + st * L::kTile + c * kPanelBytes, &tm_v, &bar_v_full[st],
-                                    c * 64, g, seg0 + j * 128);
+                                    c * 64, g, seg0 + kv_tile(j) * 128);
                     vpar[st] = (j >> 1) & 1;
                     ++vfill;
                 }
@@ -222,33 +252,49 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mma_commit_warp(&bar_s_full[t]);
                     mma_commit_warp(&bar_k_empty[j & 1]);
                 };
-                bool ok = wait(bar_q, 0, 24) && wait(&bar_k_full[0], 0, 25) && my_turn();
+                // work: this tile computes in the current step (always, without a mask); ka
+                // counts those steps, which its own barriers' phases follow, while the K/V
+                // stages' phases follow the step itself
+                bool work = has_work(t, 0);
+                bool ok = wait(bar_q, 0, 24) && (!work || wait(&bar_k_full[0], 0, 25)) && my_turn();
                 if (ok) {
-                    tc_fence_after();
-                    issue_s(0);
+                    if (work) {
+                        tc_fence_after();
+                        issue_s(0);
+                    }
                     publish(++nb);
                 }
+                int ka = 0;
                 for (int j = 0; j < nk && ok; ++j) {
                     const int st = j & 1;
+                    const bool next = j + 1 < nk && has_work(t, j + 1);
+                    if (kMask && !work && !wait(&bar_k_full[st], (j >> 1) & 1, 25)) break;
                     if (!wait(&bar_v_full[st], (j >> 1) & 1, 26)) break;
-                    if (j + 1 < nk && !wait(&bar_k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 28)) break;
-                    if (!wait(&bar_p_half[t], j & 1, 18)) break;
+                    if (next && !wait(&bar_k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 28)) break;
+                    if (work && !wait(&bar_p_half[t], ka & 1, 18)) break;
                     if (!my_turn()) break;
-                    // P.V over the first 64 keys while the softmax finishes the second half
                     tc_fence_after();
-                    const uint32_t va = s_base + L::kV + st * L::kTile;
+                    if (work) {
+                        // P.V over the first 64 keys while the softmax finishes the second half
+                        const uint32_t va = s_base + L::kV + st * L::kTile;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ts_warp(t_o, t_s + k * 8, desc_mnmajor(va, k), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
-                    if (!wait(&bar_p_ready[t], j & 1, 27)) break;
-                    tc_fence_after();
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ts_warp(t_o, t_s + k * 8, desc_mnmajor(va, k), kIdescO, (ka > 0 || k > 0) ? 1u : 0u);
+                        if (!wait(&bar_p_ready[t], ka & 1, 27)) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 4; k < 8; ++k)
-                        mma_bf16_ts_warp(t_o, t_s + k * 8, desc_mnmajor(va, k), kIdescO, 1u);
-                    mma_commit_warp(&bar_o_done[t]);
-                    mma_commit_warp(&bar_v_empty[st]);
-                    if (j + 1 < nk) issue_s(j + 1);
+                        for (int k = 4; k < 8; ++k)
+                            mma_bf16_ts_warp(t_o, t_s + k * 8, desc_mnmajor(va, k), kIdescO, 1u);
+                        mma_commit_warp(&bar_o_done[t]);
+                        mma_commit_warp(&bar_v_empty[st]);
+                        ++ka;
+                    } else {
+                        mma_commit_warp(&bar_k_empty[st]);   // nothing of this tile reads the stages
+                        mma_commit_warp(&bar_v_empty[st]);
+                    }
+                    if (next) issue_s(j + 1);
                     publish(++nb);
+                    work = next;
                 }
                 publish(INT_MAX);   // finished (or aborted): never hold the other issuer
                 mma_commit_warp(&bar_done[t]);
@@ -269,8 +315,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int q_local = qt * 128 + r;
         float m_ref = -INFINITY, l_run = 0.f;
         bool failed = false;
-        for (int j = 0; j < nk; ++j) {
-            const bool got = mbar_wait_or_abort(&bar_s_full[t], j & 1, 30, abort_flag);
+        // raw scores are scaled in the exponent's FMA; capped ones come scaled
+        const float to_log2 = kCap ? 1.f : prm.scale_log2;
+        // the row's visible keys: [0, see_prefix) and [see_from, see_to]
+        int see_prefix = 0, see_from = 0, see_to = 0;
+        // keys that every row of the tile sees: below all_prefix, and from all_from to the diagonal
+        int all_prefix = 0, all_from = 0;
+        if constexpr (kMask) {
+            see_to = min(q_local, len - 1);
+            see_prefix = prm.mod.prefix_causal ? min(P, see_to + 1) : P;
+            all_prefix = prm.mod.prefix_causal ? min(P, qt * 128 + 1) : P;
+            if (prm.mod.row_start && nk > 0) {
+                const int32_t* rs = prm.mod.row_start + seg0;
+                const int from = rs[see_to];
+                // starts lie in the row's own past and never decrease
+                if (from < 0 || from > see_to || (see_to + 1 < len && rs[see_to + 1] < from))
+                    report_error(16, kErrBadMask);
+                see_from = min(max(from, 0), see_to);
+                all_from = min(max(rs[min(qt * 128 + 127, len - 1)], 0), len - 1);
+            }
+        }
+        float bias = 0.f;   // per key of distance, in the scores' units
+        bool two_sided = false;
+        if constexpr (kBias) {
+            bias = prm.mod.slopes[h] * (kCap ? -1.4426950408889634f : -1.4426950408889634f / prm.scale_log2);
+            two_sided = !prm.causal || (kMask && P > 0 && !prm.mod.prefix_causal);
+        }
+        int ka = 0;   // steps with work so far
+        for (int step = 0; step < nk; ++step) {
+            if (kMask && !has_work(t, step)) continue;
+            const int j = kv_tile(step);
+            const bool got = mbar_wait_or_abort(&bar_s_full[t], ka & 1, 30, abort_flag);
             if (!__all_sync(0xffffffffu, got)) { failed = true; break; }
             tc_fence_after();
             // the row's 128 score columns: eight loads in flight, one wait
@@ -288,14 +363,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             }
             const int kv0 = j * 128;
-            const bool diag = prm.causal && j == qt;
-            const bool tail = kv0 + 128 > len;
-            if (diag || tail) {
+            if constexpr (kCap) cap_scores(prm.mod, sv);
+            if constexpr (kBias) {
+                // the distances t - u are exact in fp32 (below 2^24; relative to that beyond)
+                const float base = static_cast<float>(q_local - kv0);
+                if (two_sided && j >= qt) {
 #pragma unroll
-                for (int e = 0; e < 128; ++e) {
-                    const int kv = kv0 + e;
-                    const bool valid = !(diag && kv > q_local) && kv < len;
-                    sv[e] = valid ? sv[e] : -INFINITY;
+                    for (int e = 0; e < 128; ++e) sv[e] = fmaf(fabsf(base - e), bias, sv[e]);
+                } else {
+                    const float2 b2 = make_float2(base, base), s2 = make_float2(bias, bias);
+#pragma unroll
+                    for (int e = 0; e < 128; e += 2) {
+                        const float2 x = f2_fma(f2_add(b2, make_float2(-e, -e - 1)), s2, make_float2(sv[e], sv[e + 1]));
+                        sv[e] = x.x;
+                        sv[e + 1] = x.y;
+                    }
+                }
+            }
+            if constexpr (kMask) {
+                const bool whole = kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt);
+                if (!whole) {
+                    const int pre = see_prefix - kv0, from = see_from - kv0, to = see_to - kv0;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e) sv[e] = (e < pre || (e >= from && e <= to)) ? sv[e] : -INFINITY;
+                }
+            } else {
+                const bool diag = prm.causal && j == qt;
+                const bool tail = kv0 + 128 > len;
+                if (diag || tail) {
+#pragma unroll
+                    for (int e = 0; e < 128; ++e) {
+                        const int kv = kv0 + e;
+                        const bool valid = !(diag && kv > q_local) && kv < len;
+                        sv[e] = valid ? sv[e] : -INFINITY;
+                    }
                 }
             }
             // row maximum of the raw scores (three-input maxima, four independent chains);
@@ -306,11 +407,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mq[q] = fmax3(mq[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
             }
-            const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * prm.scale_log2;
+            const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * to_log2;
             // stale-max rule: keep the old reference unless the row maximum grew a lot
             float alpha = 1.f;
             bool rescale = false;
-            if (j == 0) {
+            if (ka == 0) {
                 m_ref = mx;
             } else if (mx > m_ref + kRescaleThreshold) {
                 alpha = fast_exp2(m_ref - mx);
@@ -320,7 +421,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (__any_sync(0xffffffffu, rescale)) {
                 // O_t must hold the previous P.V product before it is rescaled (it does: S
                 // of this step completed after it); no P.V of this step has started yet
-                const bool got_o = mbar_wait_or_abort(&bar_o_done[t], (j - 1) & 1, 31, abort_flag);
+                const bool got_o = mbar_wait_or_abort(&bar_o_done[t], (ka - 1) & 1, 31, abort_flag);
                 if (!__all_sync(0xffffffffu, got_o)) { failed = true; break; }
                 tc_fence_after();
 #pragma unroll
@@ -335,9 +436,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // P = 2^(scale * S - m_ref), in four chunks of 32 columns, software-pipelined:
             // the exponentials of chunk c+1 are issued ahead of the row sums, the bf16
             // packing and the TMEM store of chunk c, so that one warp keeps the MUFU busy
-            const float neg_m = -m_ref;
+            // (a row that has seen no key yet keeps the reference -inf and gets P = 0)
+            const float neg_m = kMask && m_ref == -INFINITY ? 0.f : -m_ref;
             // (scale and subtract, and the row sums, in packed pairs)
-            const float2 sc2 = make_float2(prm.scale_log2, prm.scale_log2);
+            const float2 sc2 = make_float2(to_log2, to_log2);
             const float2 nm2 = make_float2(neg_m, neg_m);
             auto exps = [&](int c, float (&p)[32]) {
 #pragma unroll
@@ -380,10 +482,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar_p_ready[t]);
+            ++ka;
         }
         // ---- epilogue: O / l -> bf16, LSE ----
         bool have = !failed && nk > 0 && !*abort_flag;
-        if (have) have = mbar_wait_or_abort(&bar_o_done[t], (nk - 1) & 1, 32, abort_flag);
+        if (have) have = mbar_wait_or_abort(&bar_o_done[t], (ka - 1) & 1, 32, abort_flag);
         have = __all_sync(0xffffffffu, have);
         if (have) {
             tc_fence_after();

@@ -1,0 +1,128 @@
+// Modified scores: what the attention kernels do to S = <q_t, k_u> between the two matrix
+// products.  In units of log2 (the softmax runs in the exp2 domain), with s2 = scale log2 e:
+//   y = C tanh(S a), a = scale / cap, C = cap log2 e       (kCap; else y = S s2)
+//   z = y - slope_h log2(e) |t - u|                        (kBias)
+//   z = -inf unless the mask lets row t see key u          (kMask)
+// and in the gradient dy = P (dP - D), dS = dy (1 - (y / C)^2) scale.
+//
+// Mask, per segment, rows and keys counted from its start: a row t sees its own keys
+// [row_start[t], t] and the prefix keys u < P (with prefix_causal only those u <= t).
+// row_start never decreases, which is what makes the tiles that a query tile needs two runs
+// (the prefix, and a run that ends at the diagonal), and the rows that see a key one run.
+#pragma once
+
+#include "lf_device.cuh"
+
+namespace lf {
+
+enum { kModCap = 1, kModBias = 2, kModMask = 4 };
+
+// tanh(x) = x p(x^2) on |x| <= kCapRange: p is the relative minimax fit of degree five
+// (iterated weighted least squares on Chebyshev nodes, in double), off by 2.9e-8 of tanh
+// in exact arithmetic and by 1.6e-7 in fp32.  Beyond, 1 - 2 / (1 + exp(2 |x|)), whose
+// error is below 4e-7 of tanh there.  tanh.approx (2^-11) would cost the scores 3 digits.
+constexpr float kCapRange = 0.75f;
+constexpr int kCapTerms = 6;
+constexpr double kCapCoef[kCapTerms] = {0.999999971014, -0.333329588792, 0.133254060138,
+                                        -0.053344429950, 0.019582907796, -0.004716256973};
+
+struct ModParams {
+    float cap_in;                // a
+    float cap_out_inv;           // 1 / C
+    float cap_out;               // C
+    float cap_coef[kCapTerms];   // C times the fit's coefficients
+    const float* slopes;         // [hq]
+    const int32_t* prefix;       // [nseq], or null
+    int prefix_causal;
+    const int32_t* row_start;    // [T], or null
+};
+
+// C tanh(a s) of a pair, |a s| <= kCapRange.
+__device__ __forceinline__ float2 cap_near(const ModParams& m, float2 s) {
+    const float2 x = f2_mul(s, make_float2(m.cap_in, m.cap_in));
+    const float2 w = f2_mul(x, x);
+    float2 p = make_float2(m.cap_coef[kCapTerms - 1], m.cap_coef[kCapTerms - 1]);
+#pragma unroll
+    for (int i = kCapTerms - 2; i >= 0; --i) p = f2_fma(p, w, make_float2(m.cap_coef[i], m.cap_coef[i]));
+    return f2_mul(p, x);
+}
+// The same for any s.
+__device__ __forceinline__ float cap_far(const ModParams& m, float s) {
+    const float x = s * m.cap_in;
+    const float e = fast_exp2(fabsf(x) * 2.8853900817779268f);   // exp(2 |x|); inf is fine
+    return copysignf(fmaf(-2.f * m.cap_out, __fdividef(1.f, 1.f + e), m.cap_out), x);
+}
+__device__ __forceinline__ float2 cap_any(const ModParams& m, float2 s) {
+    const float2 y = cap_near(m, s);
+    const float lim = kCapRange;
+    return make_float2(fabsf(s.x * m.cap_in) <= lim ? y.x : cap_far(m, s.x),
+                       fabsf(s.y * m.cap_in) <= lim ? y.y : cap_far(m, s.y));
+}
+
+// The cap over a thread's 128 scores; the warp takes the short path when all of its scores
+// lie in the fit's range, which scores far below the cap do.
+__device__ __forceinline__ void cap_scores(const ModParams& m, float (&s)[128]) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 128; e += 2) top = fmax3(top, fabsf(s[e]), fabsf(s[e + 1]));
+    if (__any_sync(0xffffffffu, !(top * m.cap_in <= kCapRange))) {
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) {
+            const float2 y = cap_any(m, make_float2(s[e], s[e + 1]));
+            s[e] = y.x;
+            s[e + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) {
+            const float2 y = cap_near(m, make_float2(s[e], s[e + 1]));
+            s[e] = y.x;
+            s[e + 1] = y.y;
+        }
+    }
+}
+
+// The prefix length of segment s within its length.
+__device__ __forceinline__ int prefix_of(const ModParams& m, int s, int len, bool& bad) {
+    if (!m.prefix) return 0;
+    const int p = m.prefix[s];
+    bad = p < 0;
+    return min(max(p, 0), len);
+}
+
+// The KV tiles that a pair of query tiles (2m, 2m+1) visits, in order: step i is KV tile
+// i for i < n_prefix, then lo, lo + 1, ...  A query tile takes part in the steps whose tile
+// lies in its own runs [0, np) and [lo, hi).
+struct PairSteps {
+    int n_prefix, lo;
+    __device__ int tile(int i) const { return i < n_prefix ? i : lo + i - n_prefix; }
+};
+struct TileRuns {
+    int np, lo, hi;
+    __device__ bool has(int j) const { return j < np || (j >= lo && j < hi); }
+    // one past the last step with work for this tile
+    __device__ int steps(const PairSteps& p) const {
+        return hi > p.lo ? p.n_prefix + hi - p.lo : max(np, hi);
+    }
+};
+__device__ __forceinline__ TileRuns tile_runs(const ModParams& m, int qt, int seg0, int len, int P) {
+    const int q0 = qt * 128;
+    TileRuns r;
+    const int seen = m.prefix_causal ? min(P, min(q0 + 128, len)) : P;
+    r.np = (seen + 127) >> 7;
+    r.lo = m.row_start ? min(max(m.row_start[seg0 + q0], 0), q0) >> 7 : 0;
+    r.hi = qt + 1;
+    return r;
+}
+
+// Last row of the segment that sees key u as its own: rows' starts ascend, so a bisection.
+__device__ __forceinline__ int last_row_of_key(const int32_t* row_start, int seg0, int len, int u) {
+    int lo = u, hi = len;   // the first row with a start behind u lies in (lo, hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (row_start[seg0 + mid] <= u) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace lf

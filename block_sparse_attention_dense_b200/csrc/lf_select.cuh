@@ -11,6 +11,7 @@
 #pragma once
 
 #include "lf_device.cuh"
+#include "lf_mod.cuh"
 
 namespace lf {
 
@@ -463,12 +464,16 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float4* __restric
 // Prologue: zero the kept blocks' accumulator rows and, when Dw is given (the caller
 // passed no D), compute D = <dO_t, O_t> for the kept blocks' rows and write 0 for the
 // dropped blocks' rows (the backward reads them, with weight 0, when a 128-row tile
-// holds one kept and one dropped 64-row block).
+// holds one kept and one dropped 64-row block).  With key_last (modified scores with
+// per-row starts) the head-0 CTAs also find, for each of the block's keys, the last row of
+// the segment that sees it: one bisection per key, here rather than in the backward's CTAs,
+// each of which would repeat it for every head group.
 template <int D>
 __global__ void __launch_bounds__(kNormThreads) bwd_prologue_kernel(
     const int32_t* __restrict__ cu_seqlens, int T, int max_seqlen, int H, int block_q, int nbmax,
     const float* __restrict__ w, float* __restrict__ acc, const __nv_bfloat16* __restrict__ dout,
-    const __nv_bfloat16* __restrict__ o, float* __restrict__ Dw) {
+    const __nv_bfloat16* __restrict__ o, float* __restrict__ Dw, const int32_t* __restrict__ row_start,
+    int32_t* __restrict__ key_last) {
     const int b = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
     int seg0, len;
     if (!load_segment(cu_seqlens, s, T, max_seqlen, seg0, len, 50)) return;
@@ -479,6 +484,10 @@ __global__ void __launch_bounds__(kNormThreads) bwd_prologue_kernel(
         float4* dst = reinterpret_cast<float4*>(acc + ((size_t)h * T + seg0 + r0) * D);
         const int n4 = (r1 - r0) * D / 4;
         for (int i = threadIdx.x; i < n4; i += blockDim.x) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (key_last && h == 0) {
+        for (int u = r0 + threadIdx.x; u < r1; u += blockDim.x)
+            key_last[seg0 + u] = last_row_of_key(row_start, seg0, len, u);
     }
     if (Dw) {
         if (kept) {

@@ -220,6 +220,52 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
                                 void* dk, void* dv, lf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Attention with modified scores (no counterpart in the article; the forward and the
+ * block-sparse backward of models that cap or bias their scores, or whose rows do not
+ * see all earlier keys).
+ *
+ *   z(t, u) = cap(softmax_scale * <q_t, k_u>) - slope_h * |t - u|,
+ *   cap(x) = softcap * tanh(x / softcap),  and -inf where row t does not see key u.
+ *
+ * Rows and keys are counted from their segment's start.  Row t sees
+ *   its own keys     row_start[t] <= u <= t   (without row_start: u <= t), and
+ *   the prefix keys  u < prefix_len[s]        (with prefix_causal only those u <= t).
+ * So: prefix_len alone is a prefix mask (the prefix is seen whole, also by its own rows);
+ * row_start[t] = start of t's document is a document mask; row_start[t] = max(0, t - w + 1)
+ * is a window of w keys, with prefix_causal and a prefix of n keys that stay visible; and a
+ * prompt of P tokens followed by its answers, row_start[t] = start of t's answer (0 in the
+ * prompt), prefix_len = P, prefix_causal = 1, is a batch that shares its prompt: the
+ * prompt's rows, K and V are computed once, and its dK and dV gather all answers' gradients.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    float softcap;               /* 0: none; else in [1e-3, 1e6] */
+    const float* alibi_slopes;   /* DEVICE [hq], or NULL: no bias.  No gradient is computed for it.  The
+                                    distance counts rows of the packed segment */
+    const int32_t* prefix_len;   /* DEVICE [nseq], >= 0 (beyond the segment: the whole segment), or NULL */
+    int32_t prefix_causal;       /* 0 or 1 (1 only with prefix_len) */
+    const int32_t* row_start;    /* DEVICE [total_tokens], or NULL.  Within a segment 0 <= row_start[t] <= t,
+                                    and it never decreases: every row sees itself.  Not read outside
+                                    segments */
+} lf_score_mod;
+
+/* lf_attn_fwd and lf_attn_bwd with modified scores.  Arguments, results, workspace
+ * (lf_workspace_size) and errors are theirs; the selection between the two is
+ * lf_block_select's.  prefix_len and row_start need causal = 1 (LF_ERR_UNSUPPORTED
+ * otherwise).  Device arrays of the modifier need only their type's alignment; their contents are
+ * checked on the device by the forward (a negative prefix by both): one that breaks its
+ * rule is reported by the next call (LF_ERR_INVALID_ARG), with the results undefined.
+ * Only the KV tiles that a row tile sees are loaded, and only the kept query tiles that
+ * see a KV tile are visited. */
+lf_status lf_attn_fwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                          const void* k, const void* v, void* o, float* lse, void* ws,
+                          size_t ws_bytes, lf_stream_t stream);
+lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
+                          const void* k, const void* v, const void* o, const float* lse,
+                          const void* dout, const float* D, const float* block_weight,
+                          const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
+                          void* dv, void* ws, size_t ws_bytes, lf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Norms of the query and key heads with the position rotation (no counterpart in
  * the article: the step between a layer's projections and its attention in models
  * that normalise their heads, such as the article's).
