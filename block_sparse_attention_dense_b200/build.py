@@ -17,7 +17,6 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared",
     "--diag-suppress", "177",
-    "--split-compile=0",   # the kernel variants compile side by side
 ]
 
 

@@ -163,7 +163,7 @@ lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void*
         !make_thd_map(&mk, k, d->total_tokens, d->hkv, D) ||
         !make_thd_map(&mv, v, d->total_tokens, d->hkv, D))
         return LF_ERR_CUDA;
-    lf::FwdParams p{};
+    lf::FwdParamsOf<kMod> p{};
     p.cu_seqlens = d->cu_seqlens;
     p.T = d->total_tokens;
     p.hq = d->hq;
@@ -174,7 +174,7 @@ lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void*
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.mod = mod_params(d, mod);
+    if constexpr (kMod != 0) p.mod = mod_params(d, mod);
     const uint32_t smem = lf::FwdSmem<D>::kAlloc;
     if (cudaFuncSetAttribute(lf::attn_fwd_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
@@ -269,7 +269,7 @@ lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* ke
         mod ? mod->row_start : nullptr, key_last);
     if (launch_status() != LF_OK) return LF_ERR_CUDA;
     const float* Dv = Dgiven ? Dgiven : Dw;
-    lf::BwdParams p{};
+    lf::BwdParamsOf<kMod> p{};
     p.cu_seqlens = d->cu_seqlens;
     p.T = d->total_tokens;
     p.hq = d->hq;
@@ -290,8 +290,10 @@ lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* ke
     p.kept_idx = kidx;
     p.kept_cnt = kcnt;
     p.dq_acc = dq_acc;
-    p.mod = mod_params(d, mod);
-    p.key_last = key_last;
+    if constexpr (kMod != 0) {
+        p.mod = mod_params(d, mod);
+        p.key_last = key_last;
+    }
     const uint32_t smem = lf::BwdSmem<D>::kAlloc;
     // 64-row selection blocks: the variant that skips a tile's dropped half
     auto kern = d->block_q == 64 ? lf::attn_bwd_kernel<D, true, kMod> : lf::attn_bwd_kernel<D, false, kMod>;

@@ -52,6 +52,8 @@
 // issue order.
 #pragma once
 
+#include <type_traits>
+
 #include "lf_device.cuh"
 #include "lf_mod.cuh"
 
@@ -79,9 +81,16 @@ struct BwdParams {
     int tile_major;
     __nv_bfloat16* dk_out;
     __nv_bfloat16* dv_out;
-    ModParams mod;             // read where kMod is not 0
+};
+// ... of the variants with modified scores.  A type of its own: the mere presence of these
+// fields in the plain kernel's parameters changed its register allocation (2.5 % slower at
+// 32K tokens, A/B on one GPU).
+struct BwdModParams : BwdParams {
+    ModParams mod;
     const int32_t* key_last;   // [T] last row of the segment that sees the key, with mod.row_start
 };
+template <int kMod>
+using BwdParamsOf = std::conditional_t<kMod == 0, BwdParams, BwdModParams>;
 
 constexpr uint32_t kAccBox = 128 * 32 * 4;   // one staged 32-column fp32 box of a KV tile
 constexpr int kMaxHeadsPerCta = 32;           // query heads one backward CTA can walk
@@ -134,15 +143,16 @@ __device__ __forceinline__ int lower_bound_warp(const int32_t* list, int cnt, in
 }
 
 // Before the walk, the warps of the CTA find, head by head (warp w takes heads w,
-// w + 16, ...), each head's first kept block at or after the CTA's first query row
-// with the warp-parallel search, and store (position, end) in shared memory; the
+// w + 16, ...), each head's first kept block at or after the CTA's first query tile
+// with the warp-parallel search, and store (position, count) in shared memory; the
 // return value says whether that head has any tile to visit (the same on every lane).
-// kMask: the walk also ends after the block of row last_row.
+// kMask: the rows that may see the CTA's keys are [first_row, last_row] of the segment;
+// the walk starts at the first one's block and ends after the last one's.
 template <bool kMask>
-__device__ __forceinline__ bool find_head_starts(const BwdParams& p, int G, int g, int s, int first_row,
-                                                 int last_row, int len, int2* heads) {
+__device__ __forceinline__ bool find_head_starts(const BwdParams& p, int G, int g, int s, int jt,
+                                                 int len, int2* heads, int first_row, int last_row) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first_block = first_row / p.block_q;
+    const int first_block = kMask ? first_row / p.block_q : p.causal ? (jt * 128) / p.block_q : 0;
     const int nb = (len + p.block_q - 1) / p.block_q;
     bool any = false;
     for (int hh = warp; hh < G; hh += kBwdThreads / 32) {
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_dvacc, const __grid_constant__ CUtensorMap tm_dkacc,
                     const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_do64,
-                    BwdParams prm) {
+                    BwdParamsOf<kMod> prm) {
     using L = BwdSmem<D>;
     constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
     static_assert(2 * (D / 32) * kAccBox <= 4 * L::kTile, "dK/dV staging must fit the Q/dO buffers");
@@ -303,8 +313,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // every head's first kept tile for this KV tile; does the tile have any work?
     int2* head_starts = reinterpret_cast<int2*>(smem + L::kHeads);
     // the rows that may see the tile's keys: from first_row (0 for a prefix seen whole) to last_row
-    int first_row = prm.causal ? jt * 128 : 0, last_row = len - 1, P = 0;
+    int first_row = 0, last_row = 0, P = 0;
     if constexpr (kMask) {
+        first_row = jt * 128;
+        last_row = len - 1;
         bool bad = false;
         P = prefix_of(prm.mod, s, len, bad);
         if (bad && tid == 0) report_error(18, kErrBadMask);
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (in_prefix && !prm.mod.prefix_causal) first_row = 0;
         if (!in_prefix && prm.mod.row_start) last_row = prm.key_last[seg0 + min(jt * 128 + 127, len - 1)];
     }
-    const bool has = find_head_starts<kMask>(prm, prm.heads_per_cta, hgrp, s, first_row, last_row, len, head_starts);
+    const bool has = find_head_starts<kMask>(prm, prm.heads_per_cta, hgrp, s, jt, len, head_starts, first_row, last_row);
     float* slopes_s = reinterpret_cast<float*>(smem + L::kSlopes);   // -slope log2(e) per query head
     if constexpr (kBias) {
         if (tid < prm.heads_per_cta)
@@ -673,8 +685,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 x = f2_fma(make_float2(fabsf(dist.x), fabsf(dist.y)), make_float2(slope, slope), x);
                             }
                             float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                            if (kv_cmp > q0 + col0 + u || (kMask && q_last < q0 + col0 + u)) p0 = 0.f;
-                            if (kv_cmp > q0 + col0 + u + 1 || (kMask && q_last < q0 + col0 + u + 1)) p1 = 0.f;
+                            if (kv_cmp > q0 + col0 + u) p0 = 0.f;
+                            if (kv_cmp > q0 + col0 + u + 1) p1 = 0.f;
+                            if constexpr (kMask) {
+                                if (q_last < q0 + col0 + u) p0 = 0.f;
+                                if (q_last < q0 + col0 + u + 1) p1 = 0.f;
+                            }
                             const float2 pw2 = f2_mul(make_float2(p0, p1), w2);
                             float2 ds2 = f2_mul(pw2, f2_sub(dp2, dv2));
                             if constexpr (kCap) ds2 = f2_mul(ds2, damp);

@@ -32,6 +32,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "lf_device.cuh"
 #include "lf_mod.cuh"
@@ -45,8 +46,12 @@ struct FwdParams {
     int tile_major;            // CTA order: 1 = KV head fastest (see the kernel)
     __nv_bfloat16* o;
     float* lse;
-    ModParams mod;             // read where kMod is not 0
 };
+struct FwdModParams : FwdParams {
+    ModParams mod;
+};
+template <int kMod>
+using FwdParamsOf = std::conditional_t<kMod == 0, FwdParams, FwdModParams>;
 
 template <int D>
 struct FwdSmem {
@@ -69,7 +74,7 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a re
 template <int D, int kMod>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, FwdParams prm) {
+                    const __grid_constant__ CUtensorMap tm_v, FwdParamsOf<kMod> prm) {
     using L = FwdSmem<D>;
     constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
     extern __shared__ uint8_t smem_raw[];
