@@ -145,8 +145,13 @@ lf::ModParams mod_params(const lf_attn_desc* d, const lf_score_mod* m) {
         const double c = m->softcap * 1.4426950408889634;
         p.cap_in = static_cast<float>((double)d->softmax_scale / m->softcap);
         p.cap_out = static_cast<float>(c);
-        p.cap_out_inv = static_cast<float>(1.0 / c);
+        p.cap_damp = static_cast<float>(-1.0 / (c * c));
         for (int i = 0; i < lf::kCapTerms; ++i) p.cap_coef[i] = static_cast<float>(c * lf::kCapCoef[i]);
+        const double a = (double)d->softmax_scale / m->softcap;
+        const bool fits = a >= 1e-5 && a <= 1e4;   // every C a^(2k+1) is a normal number
+        for (int i = 0; i < lf::kCapFusedTerms; ++i)
+            p.cap_fused[i] = fits ? static_cast<float>(c * lf::kCapFused[i] * std::pow(a, 2 * i + 1)) : 0.f;
+        p.fused_max = fits ? static_cast<float>(lf::kCapFusedRange / a) : 0.f;
     }
     p.slopes = m->alibi_slopes;
     p.prefix = m->prefix_len;

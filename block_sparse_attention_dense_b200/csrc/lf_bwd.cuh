@@ -89,6 +89,8 @@ struct BwdModParams : BwdParams {
     ModParams mod;
     const int32_t* key_last;   // [T] last row of the segment that sees the key, with mod.row_start
 };
+__device__ __forceinline__ const ModParams* mod_of(const BwdParams&) { return nullptr; }
+__device__ __forceinline__ const ModParams* mod_of(const BwdModParams& p) { return &p.mod; }
 template <int kMod>
 using BwdParamsOf = std::conditional_t<kMod == 0, BwdParams, BwdModParams>;
 
@@ -565,6 +567,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // the KV row lies past the segment's end (its key belongs to the next segment, so
         // its exponent is not bounded by this query's LSE and must not reach the products)
         int kv_cmp = !kv_valid ? 0x7fffffff : (prm.causal ? kv_local : (int)0x80000000);
+        const bool two_sided = kBias && (!prm.causal || (kMask && first_row == 0));
         int q_last = 0x7fffffff;   // kMask: P = 0 past this query index as well
         if constexpr (kMask) {
             if (kv_valid && kv_local < P) {
@@ -602,6 +605,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 continue;
             }
             const int qt = e.tile, q0 = qt * 128;
+            // the bias per key of distance (log2 units), and the sign of query - key: one sign
+            // over the tile pair, except on the diagonal where rows see later keys too
+            [[maybe_unused]] const float bias2 = kBias ? slopes_s[e.h - hgrp * prm.heads_per_cta] : 0.f;
+            [[maybe_unused]] const float dist_sign = qt < jt ? -1.f : 1.f;
+            const bool dist_both = kBias && two_sided && qt == jt;
             if (r < 64) {
                 // this warpgroup's 64 columns: [32 wg, 32 wg + 32) of each half
                 const int col = (r >> 5) * 64 + wg * 32 + (r & 31);
@@ -613,6 +621,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     dd = prm.Dvec[idx];
                 }
                 lse2_s[col] = -l2;   // stored negated: the exponent is one packed FMA
+                if constexpr (kBias) lse2_s[col] = fmaf(dist_sign * bias2, static_cast<float>(col), -l2);
                 dvec_s[col] = dd;
             }
             named_bar_sync(2, 256);
@@ -640,20 +649,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 // fp32 columns of the other)
                 named_bar_sync(3, 256);
                 if (!ok) { failed = true; continue; }
-                // distances |t - u|: column minus key, exact in fp32 (below 2^24)
-                const float dist0 = kBias ? static_cast<float>(q0 + hf * 64 - kv_local) : 0.f;
-                const float slope = kBias ? slopes_s[e.h - hgrp * prm.heads_per_cta] : 0.f;
-                auto chunk = [&](int c, const uint32_t (&sr)[16], const uint32_t (&dr)[16]) {
+                // the half's variant (warp-uniform): kWhole, every key of the warp sees every
+                // column, so nothing is compared (kMod only; the plain kernel always compares);
+                // kGeneral, capped scores outside the narrow fit, or distances of both signs
+                [[maybe_unused]] const float bias_u = kBias ? dist_sign * bias2 * static_cast<float>(q0 - kv_local) : 0.f;
+                auto chunk = [&](int c, const uint32_t (&sr)[16], const uint32_t (&dr)[16], auto variant) {
+                    constexpr bool kWhole = decltype(variant)::value == 1, kGeneral = decltype(variant)::value == 2;
                     uint32_t pk[8], dk_[8];
-                    const float dist_c = dist0 + static_cast<float>(c * 16);
-                    bool far = false;   // a capped score of the warp lies outside the fit's range
-                    if constexpr (kCap) {
-                        float top = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2)
-                            top = fmax3(top, fabsf(__uint_as_float(sr[i])), fabsf(__uint_as_float(sr[i + 1])));
-                        far = __any_sync(0xffffffffu, !(top * prm.mod.cap_in <= kCapRange));
-                    }
 #pragma unroll
                     for (int e4 = 0; e4 < 4; ++e4) {
                         const int col0 = hf * 64 + c * 16 + 4 * e4;
@@ -671,23 +673,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                                           __uint_as_float(sr[4 * e4 + u + 1]));
                             const float2 dp2 = make_float2(__uint_as_float(dr[4 * e4 + u]),
                                                            __uint_as_float(dr[4 * e4 + u + 1]));
-                            float2 x, damp = make_float2(1.f, 1.f);
+                            float2 x, damp;
                             if constexpr (kCap) {
-                                const float2 y = far ? cap_any(prm.mod, s2) : cap_near(prm.mod, s2);
-                                const float2 th = f2_mul(y, make_float2(prm.mod.cap_out_inv, prm.mod.cap_out_inv));
-                                damp = f2_fma(th, make_float2(-th.x, -th.y), damp);   // 1 - tanh^2
+                                const float2 y = kGeneral ? cap_any(*mod_of(prm), s2)
+                                                          : f2_mul(s2, cap_fused_factor(*mod_of(prm), s2));
                                 x = f2_add(y, nl);
+                                // 1 - tanh^2
+                                const float dc = mod_of(prm)->cap_damp;
+                                damp = f2_fma(f2_mul(y, y), make_float2(dc, dc), make_float2(1.f, 1.f));
                             } else {
                                 x = f2_fma(s2, sc2, nl);
                             }
                             if constexpr (kBias) {
-                                const float2 dist = f2_add(make_float2(dist_c, dist_c), make_float2(4 * e4 + u, 4 * e4 + u + 1));
-                                x = f2_fma(make_float2(fabsf(dist.x), fabsf(dist.y)), make_float2(slope, slope), x);
+                                // nl holds the columns' part of sign * (column - key)
+                                x = f2_add(x, make_float2(bias_u, bias_u));
+                                if constexpr (kGeneral) {
+                                    if (dist_both) {   // the sign differs from column to column
+                                        if (q0 + col0 + u < kv_local) x.x -= 2.f * bias2 * (q0 + col0 + u - kv_local);
+                                        if (q0 + col0 + u + 1 < kv_local) x.y -= 2.f * bias2 * (q0 + col0 + u + 1 - kv_local);
+                                    }
+                                }
                             }
                             float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                            if (kv_cmp > q0 + col0 + u) p0 = 0.f;
-                            if (kv_cmp > q0 + col0 + u + 1) p1 = 0.f;
-                            if constexpr (kMask) {
+                            if constexpr (!kWhole) {
+                                if (kv_cmp > q0 + col0 + u) p0 = 0.f;
+                                if (kv_cmp > q0 + col0 + u + 1) p1 = 0.f;
+                            }
+                            if constexpr (kMask && !kWhole) {
                                 if (q_last < q0 + col0 + u) p0 = 0.f;
                                 if (q_last < q0 + col0 + u + 1) p1 = 0.f;
                             }
@@ -709,8 +721,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     st_shared_v4(dsa + sw128_chunk_offset(r, 2 * c), dk_[0], dk_[1], dk_[2], dk_[3]);
                     st_shared_v4(dsa + sw128_chunk_offset(r, 2 * c + 1), dk_[4], dk_[5], dk_[6], dk_[7]);
                 };
-                chunk(2 * wg, sa, da);
-                chunk(2 * wg + 1, sb, db);
+                auto chunks = [&](auto variant) {
+                    chunk(2 * wg, sa, da, variant);
+                    chunk(2 * wg + 1, sb, db, variant);
+                };
+                if constexpr (kMod == 0) {
+                    chunks(std::integral_constant<int, 0>{});
+                } else {
+                    const int qh = q0 + hf * 64;
+                    bool general = dist_both;
+                    if constexpr (kCap) {
+                        float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            t0 = fmax3(t0, fabsf(__uint_as_float(sa[i])), fabsf(__uint_as_float(sa[i + 1])));
+                            t1 = fmax3(t1, fabsf(__uint_as_float(sb[i])), fabsf(__uint_as_float(sb[i + 1])));
+                        }
+                        general = general || __any_sync(0xffffffffu, !(fmaxf(t0, t1) <= prm.mod.fused_max));
+                    }
+                    if (general)
+                        chunks(std::integral_constant<int, 2>{});
+                    else if (__all_sync(0xffffffffu, kv_cmp <= qh && (!kMask || q_last >= qh + 63)))
+                        chunks(std::integral_constant<int, 1>{});
+                    else
+                        chunks(std::integral_constant<int, 0>{});
+                }
                 tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before();

@@ -50,6 +50,8 @@ struct FwdParams {
 struct FwdModParams : FwdParams {
     ModParams mod;
 };
+__device__ __forceinline__ const ModParams* mod_of(const FwdParams&) { return nullptr; }
+__device__ __forceinline__ const ModParams* mod_of(const FwdModParams& p) { return &p.mod; }
 template <int kMod>
 using FwdParamsOf = std::conditional_t<kMod == 0, FwdParams, FwdModParams>;
 
@@ -70,6 +72,7 @@ constexpr int kFwdLaunchRegs = 168;     // 65536 / 384, rounded down to a multip
 constexpr int kFwdCtrlRegs = 64;
 constexpr int kFwdSoftmaxRegs = 216;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a rescale
+constexpr float kFusedSpread = 64.0f;       // log2 of how far below 1 a row's largest P may lie
 
 template <int D, int kMod>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -134,18 +137,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (bad && threadIdx.x == 0) report_error(17, kErrBadMask);
         runs0 = tile_runs(prm.mod, 2 * m, seg0, len, P);
         runs1 = two ? tile_runs(prm.mod, 2 * m + 1, seg0, len, P) : TileRuns{0, 0, 0};
+        runs1.lo = max(runs1.lo, runs0.lo);   // starts never decrease; all roles rely on it
         steps.n_prefix = max(runs0.np, runs1.np);
         steps.lo = max(runs0.lo, steps.n_prefix);
         nkv0 = runs0.steps(steps);
         nkv1 = two ? runs1.steps(steps) : 0;
     }
     const int nkv = nkv0 > nkv1 ? nkv0 : nkv1;
-    // the KV tile of step i, and whether query tile t has work there
-    auto kv_tile = [&](int i) { return kMask ? steps.tile(i) : i; };
-    auto has_work = [&](int t, int i) {
-        if constexpr (kMask) return t ? runs1.has(steps.tile(i)) : runs0.has(steps.tile(i));
-        return true;
-    };
+    auto kv_tile = [&](int i) { return kMask ? steps.tile(i) : i; };   // of step i
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t s_base = smem_addr(smem);
@@ -260,7 +259,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // work: this tile computes in the current step (always, without a mask); ka
                 // counts those steps, which its own barriers' phases follow, while the K/V
                 // stages' phases follow the step itself
-                bool work = has_work(t, 0);
+                const int idle_from = kMask ? (t ? runs1.np : runs0.np) : 0;
+                const int idle_end = kMask ? (t ? runs1.idle_end(steps) : runs0.idle_end(steps)) : 0;
+                auto has_work = [&](int i) { return !kMask || i < idle_from || i >= idle_end; };
+                bool work = has_work(0);
                 bool ok = wait(bar_q, 0, 24) && (!work || wait(&bar_k_full[0], 0, 25)) && my_turn();
                 if (ok) {
                     if (work) {
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 int ka = 0;
                 for (int j = 0; j < nk && ok; ++j) {
                     const int st = j & 1;
-                    const bool next = j + 1 < nk && has_work(t, j + 1);
+                    const bool next = j + 1 < nk && has_work(j + 1);
                     if (kMask && !work && !wait(&bar_k_full[st], (j >> 1) & 1, 25)) break;
                     if (!wait(&bar_v_full[st], (j >> 1) & 1, 26)) break;
                     if (next && !wait(&bar_k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 28)) break;
@@ -320,36 +322,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int q_local = qt * 128 + r;
         float m_ref = -INFINITY, l_run = 0.f;
         bool failed = false;
-        // raw scores are scaled in the exponent's FMA; capped ones come scaled
-        const float to_log2 = kCap ? 1.f : prm.scale_log2;
-        // the row's visible keys: [0, see_prefix) and [see_from, see_to]
-        int see_prefix = 0, see_from = 0, see_to = 0;
-        // keys that every row of the tile sees: below all_prefix, and from all_from to the diagonal
-        int all_prefix = 0, all_from = 0;
+        int P_row = 0, from = 0;      // kMask: the prefix length, the row's first own key
+        int all_prefix = 0, all_from = 0;   // keys that every row of the tile sees: below
+                                            // all_prefix, and from all_from to the diagonal
+        TileRuns runs{};
         if constexpr (kMask) {
-            see_to = min(q_local, len - 1);
-            see_prefix = prm.mod.prefix_causal ? min(P, see_to + 1) : P;
+            runs = t ? runs1 : runs0;
+            P_row = P;
             all_prefix = prm.mod.prefix_causal ? min(P, qt * 128 + 1) : P;
             if (prm.mod.row_start && nk > 0) {
                 const int32_t* rs = prm.mod.row_start + seg0;
-                const int from = rs[see_to];
+                const int row = min(q_local, len - 1);
+                from = rs[row];
                 // starts lie in the row's own past and never decrease
-                if (from < 0 || from > see_to || (see_to + 1 < len && rs[see_to + 1] < from))
-                    report_error(16, kErrBadMask);
-                see_from = min(max(from, 0), see_to);
+                if (from < 0 || from > row || (row + 1 < len && rs[row + 1] < from)) report_error(16, kErrBadMask);
+                from = min(max(from, 0), row);
                 all_from = min(max(rs[min(qt * 128 + 127, len - 1)], 0), len - 1);
             }
         }
-        float bias = 0.f;   // per key of distance, in the scores' units
+        float bias2 = 0.f;   // per key of distance, in log2 units
         bool two_sided = false;
         if constexpr (kBias) {
-            bias = prm.mod.slopes[h] * (kCap ? -1.4426950408889634f : -1.4426950408889634f / prm.scale_log2);
+            bias2 = prm.mod.slopes[h] * -1.4426950408889634f;
             two_sided = !prm.causal || (kMask && P > 0 && !prm.mod.prefix_causal);
         }
+        // the bias of the columns within eight, by pairs
+        float2 bias_in8[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias_in8[i] = make_float2(-bias2 * (2 * i), -bias2 * (2 * i + 1));
         int ka = 0;   // steps with work so far
-        for (int step = 0; step < nk; ++step) {
-            if (kMask && !has_work(t, step)) continue;
-            const int j = kv_tile(step);
+        // the tile's KV tiles in order: all of them, or under a mask its two runs
+        for (int j = kMask && runs.np == 0 ? runs.lo : 0; j < (kMask ? max(runs.np, runs.hi) : nk);
+             j = kMask && j + 1 >= runs.np ? max(j + 1, runs.lo) : j + 1) {
             const bool got = mbar_wait_or_abort(&bar_s_full[t], ka & 1, 30, abort_flag);
             if (!__all_sync(0xffffffffu, got)) { failed = true; break; }
             tc_fence_after();
@@ -368,34 +372,70 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             }
             const int kv0 = j * 128;
-            if constexpr (kCap) cap_scores(prm.mod, sv);
-            if constexpr (kBias) {
-                // the distances t - u are exact in fp32 (below 2^24; relative to that beyond)
-                const float base = static_cast<float>(q_local - kv0);
-                if (two_sided && j >= qt) {
-#pragma unroll
-                    for (int e = 0; e < 128; ++e) sv[e] = fmaf(fabsf(base - e), bias, sv[e]);
-                } else {
-                    const float2 b2 = make_float2(base, base), s2 = make_float2(bias, bias);
-#pragma unroll
-                    for (int e = 0; e < 128; e += 2) {
-                        const float2 x = f2_fma(f2_add(b2, make_float2(-e, -e - 1)), s2, make_float2(sv[e], sv[e + 1]));
-                        sv[e] = x.x;
-                        sv[e + 1] = x.y;
+            const bool diag = !kMask && prm.causal && j == qt;
+            const bool tail = !kMask && kv0 + 128 > len;
+            // every row of the tile sees every key of the step
+            const bool whole = kMask ? kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt) : !(diag || tail);
+            // fused: the cap and the bias are part of the exponents below, so that they run in
+            // the shadow of the exp2 unit; the maximum of the raw scores, capped, plus the
+            // largest bias bounds the scores from above and serves as the row's maximum.  It
+            // is high by at most the spread between the largest score and the one with the
+            // largest bias (the nearest key), so a tile with a wide spread is not fused
+            bool fused = (kCap || kBias) && whole && !(kBias && two_sided && j >= qt);
+            float mx = 0.f;
+            if constexpr (kCap || kBias) {
+                if (fused) {
+                    mx = row_max(sv);
+                    float near = bias2 <= 0.f ? sv[127] : sv[0];
+                    if constexpr (kCap) {
+                        fused = !__any_sync(0xffffffffu, !(row_max_size(sv) <= prm.mod.fused_max));
+                        mx = cap_fused_one(prm.mod, mx);
+                        if (kBias) near = cap_fused_one(prm.mod, near);
+                    } else {
+                        mx *= prm.scale_log2;
+                        near *= prm.scale_log2;
+                    }
+                    if constexpr (kBias) {
+                        fused = fused && !__any_sync(0xffffffffu, !(mx - near <= kFusedSpread));
+                        mx = fmaf(static_cast<float>(q_local - kv0 - (bias2 <= 0.f ? 127 : 0)), bias2, mx);
                     }
                 }
             }
-            if constexpr (kMask) {
-                const bool whole = kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt);
-                if (!whole) {
-                    const int pre = see_prefix - kv0, from = see_from - kv0, to = see_to - kv0;
+            if (!fused) {
+                // raw scores are scaled in the exponent's FMA; capped ones come scaled
+                const float to_log2 = kCap ? 1.f : prm.scale_log2;
+                if constexpr (kCap) cap_scores(prm.mod, sv);
+                if constexpr (kBias) {
+                    // the distances t - u are exact in fp32 (below 2^24; relative to that beyond)
+                    const float base = static_cast<float>(q_local - kv0);
+                    const float bias = kCap ? bias2 : bias2 / prm.scale_log2;
+                    if (two_sided && j >= qt) {
 #pragma unroll
-                    for (int e = 0; e < 128; ++e) sv[e] = (e < pre || (e >= from && e <= to)) ? sv[e] : -INFINITY;
+                        for (int e = 0; e < 128; ++e) sv[e] = fmaf(fabsf(base - e), bias, sv[e]);
+                    } else {
+                        const float2 b2 = make_float2(base, base), s2 = make_float2(bias, bias);
+#pragma unroll
+                        for (int e = 0; e < 128; e += 2) {
+                            const float2 x = f2_fma(f2_add(b2, make_float2(-e, -e - 1)), s2, make_float2(sv[e], sv[e + 1]));
+                            sv[e] = x.x;
+                            sv[e + 1] = x.y;
+                        }
+                    }
                 }
-            } else {
-                const bool diag = prm.causal && j == qt;
-                const bool tail = kv0 + 128 > len;
-                if (diag || tail) {
+                if constexpr (kMask) {
+                    if (!whole) {
+                        // visible: [0, pre) and [from, to] (a padding row takes the last row's)
+                        const int row = min(q_local, len - 1);
+                        const int pre = (prm.mod.prefix_causal ? min(P_row, row + 1) : P_row) - kv0;
+                        const int first = from - kv0;
+                        const unsigned own = row - from;
+                        // (one unsigned compare for [from, to]: with two, the compiler spilled
+                        // a quarter of the scores)
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            sv[e] = (e < pre || static_cast<unsigned>(e - first) <= own) ? sv[e] : -INFINITY;
+                    }
+                } else if (diag || tail) {
 #pragma unroll
                     for (int e = 0; e < 128; ++e) {
                         const int kv = kv0 + e;
@@ -403,16 +443,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         sv[e] = valid ? sv[e] : -INFINITY;
                     }
                 }
+                // row maximum of the raw scores; the scale is positive, so scaling the maximum
+                // gives the scaled maximum
+                mx = row_max(sv) * to_log2;
             }
-            // row maximum of the raw scores (three-input maxima, four independent chains);
-            // the scale is positive, so scaling the maximum gives the scaled maximum
-            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 128; e += 8) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mq[q] = fmax3(mq[q], sv[e + 2 * q], sv[e + 2 * q + 1]);
-            }
-            const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])) * to_log2;
             // stale-max rule: keep the old reference unless the row maximum grew a lot
             float alpha = 1.f;
             bool rescale = false;
@@ -444,12 +478,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // (a row that has seen no key yet keeps the reference -inf and gets P = 0)
             const float neg_m = kMask && m_ref == -INFINITY ? 0.f : -m_ref;
             // (scale and subtract, and the row sums, in packed pairs)
+            const float to_log2 = kCap ? 1.f : prm.scale_log2;
             const float2 sc2 = make_float2(to_log2, to_log2);
             const float2 nm2 = make_float2(neg_m, neg_m);
-            auto exps = [&](int c, float (&p)[32]) {
+            const float fused_base = kBias ? fmaf(static_cast<float>(q_local - kv0), bias2, neg_m) : neg_m;
+            auto exps = [&](int c, float (&p)[32], auto fuse) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float2 x = f2_fma(make_float2(sv[c * 32 + e], sv[c * 32 + e + 1]), sc2, nm2);
+                    const float2 s2 = make_float2(sv[c * 32 + e], sv[c * 32 + e + 1]);
+                    float2 x;
+                    if constexpr (decltype(fuse)::value) {
+                        float2 off = make_float2(fused_base, fused_base);
+                        if constexpr (kBias) {
+                            const float at = fmaf(static_cast<float>(-(c * 32 + e) / 8 * 8), bias2, fused_base);
+                            off = f2_add(make_float2(at, at), bias_in8[(e % 8) / 2]);
+                        }
+                        x = f2_fma(s2, kCap ? cap_fused_factor(*mod_of(prm), s2) : sc2, off);
+                    } else {
+                        x = f2_fma(s2, sc2, nm2);
+                    }
                     p[e] = fast_exp2(x.x);
                     p[e + 1] = fast_exp2(x.y);
                 }
@@ -467,20 +514,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 tmem_st16(t_s + c * 16, pk);   // P (packed) over S columns already read
             };
-            {
+            auto probabilities = [&](auto fuse) {
                 float pa[32], pb[32];
-                exps(0, pa);
-                exps(1, pb);
+                exps(0, pa, fuse);
+                exps(1, pb, fuse);
                 finish(0, pa);
-                exps(2, pa);
+                exps(2, pa, fuse);
                 finish(1, pb);
                 // the first half of P (columns [0, 64), K = 0..63 of P.V) is in TMEM
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bar_p_half[t]);
-                exps(3, pb);
+                exps(3, pb, fuse);
                 finish(2, pa);
                 finish(3, pb);
+            };
+            if constexpr (kCap || kBias) {
+                if (fused) probabilities(std::true_type{});
+                else probabilities(std::false_type{});
+            } else {
+                probabilities(std::false_type{});
             }
             const float rs_all = (rsA.x + rsA.y) + (rsB.x + rsB.y);
             l_run = l_run * alpha + rs_all;

@@ -17,25 +17,54 @@ namespace lf {
 
 enum { kModCap = 1, kModBias = 2, kModMask = 4 };
 
-// tanh(x) = x p(x^2) on |x| <= kCapRange: p is the relative minimax fit of degree five
-// (iterated weighted least squares on Chebyshev nodes, in double), off by 2.9e-8 of tanh
-// in exact arithmetic and by 1.6e-7 in fp32.  Beyond, 1 - 2 / (1 + exp(2 |x|)), whose
-// error is below 4e-7 of tanh there.  tanh.approx (2^-11) would cost the scores 3 digits.
+// tanh(x) = x p(x^2), p a relative minimax fit (iterated weighted least squares on Chebyshev
+// nodes, in double).  tanh.approx (2^-11) would cost the scores three digits, and exp and a
+// reciprocal two more operations of the unit that the softmax already fills.
+//  * kCapFused: |x| <= 1/2, degree three, off by 5.5e-7 of tanh.  The scale goes into the
+//    coefficients (C a^(2k+1) c_k, powers of s), which holds while those stay normal numbers
+//    (the host sets fused_max to 0 where they would not), and the last product into the
+//    exponent's FMA: four packed operations a pair instead of the uncapped one.
+//  * kCapCoef: |x| <= 3/4, degree five, off by 2.9e-8, and 1.6e-7 in fp32; beyond,
+//    1 - 2 / (1 + exp(2 |x|)), whose error is below 4e-7 of tanh there.
+// A warp (or, in the gradient, a chunk of 16 columns) whose scores all lie within the first
+// takes it, else the second for all of them.
+constexpr int kCapFusedTerms = 4;
+constexpr double kCapFused[kCapFusedTerms] = {0.999999455771, -0.333263179339, 0.131902965817,
+                                              -0.044402225555};
+constexpr double kCapFusedRange = 0.5;
 constexpr float kCapRange = 0.75f;
 constexpr int kCapTerms = 6;
 constexpr double kCapCoef[kCapTerms] = {0.999999971014, -0.333329588792, 0.133254060138,
                                         -0.053344429950, 0.019582907796, -0.004716256973};
 
 struct ModParams {
-    float cap_in;                // a
-    float cap_out_inv;           // 1 / C
-    float cap_out;               // C
-    float cap_coef[kCapTerms];   // C times the fit's coefficients
-    const float* slopes;         // [hq]
-    const int32_t* prefix;       // [nseq], or null
+    float cap_in;                      // a
+    float cap_damp;                    // -1 / C^2
+    float cap_out;                     // C
+    float cap_coef[kCapTerms];         // C times the wide fit's coefficients
+    float cap_fused[kCapFusedTerms];   // C a^(2k+1) times the narrow fit's
+    float fused_max;                   // the largest |s| of the narrow fit
+    const float* slopes;               // [hq]
+    const int32_t* prefix;             // [nseq], or null
     int prefix_causal;
-    const int32_t* row_start;    // [T], or null
+    const int32_t* row_start;          // [T], or null
 };
+
+// C tanh(a s) / s of a pair within the narrow fit.
+__device__ __forceinline__ float2 cap_fused_factor(const ModParams& m, float2 s) {
+    const float2 w = f2_mul(s, s);
+    float2 p = make_float2(m.cap_fused[kCapFusedTerms - 1], m.cap_fused[kCapFusedTerms - 1]);
+#pragma unroll
+    for (int i = kCapFusedTerms - 2; i >= 0; --i) p = f2_fma(p, w, make_float2(m.cap_fused[i], m.cap_fused[i]));
+    return p;
+}
+__device__ __forceinline__ float cap_fused_one(const ModParams& m, float s) {
+    const float w = s * s;
+    float p = m.cap_fused[kCapFusedTerms - 1];
+#pragma unroll
+    for (int i = kCapFusedTerms - 2; i >= 0; --i) p = fmaf(p, w, m.cap_fused[i]);
+    return p * s;
+}
 
 // C tanh(a s) of a pair, |a s| <= kCapRange.
 __device__ __forceinline__ float2 cap_near(const ModParams& m, float2 s) {
@@ -54,18 +83,34 @@ __device__ __forceinline__ float cap_far(const ModParams& m, float s) {
 }
 __device__ __forceinline__ float2 cap_any(const ModParams& m, float2 s) {
     const float2 y = cap_near(m, s);
-    const float lim = kCapRange;
-    return make_float2(fabsf(s.x * m.cap_in) <= lim ? y.x : cap_far(m, s.x),
-                       fabsf(s.y * m.cap_in) <= lim ? y.y : cap_far(m, s.y));
+    return make_float2(fabsf(s.x * m.cap_in) <= kCapRange ? y.x : cap_far(m, s.x),
+                       fabsf(s.y * m.cap_in) <= kCapRange ? y.y : cap_far(m, s.y));
 }
 
-// The cap over a thread's 128 scores; the warp takes the short path when all of its scores
-// lie in the fit's range, which scores far below the cap do.
-__device__ __forceinline__ void cap_scores(const ModParams& m, float (&s)[128]) {
-    float top = 0.f;
+// The largest value, and the largest size, of a thread's 128 scores (three-input maxima,
+// four independent chains).
+__device__ __forceinline__ float row_max(const float (&s)[128]) {
+    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < 128; e += 2) top = fmax3(top, fabsf(s[e]), fabsf(s[e + 1]));
-    if (__any_sync(0xffffffffu, !(top * m.cap_in <= kCapRange))) {
+    for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mq[q] = fmax3(mq[q], s[e + 2 * q], s[e + 2 * q + 1]);
+    }
+    return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
+}
+__device__ __forceinline__ float row_max_size(const float (&s)[128]) {
+    float mq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mq[q] = fmax3(mq[q], fabsf(s[e + 2 * q]), fabsf(s[e + 2 * q + 1]));
+    }
+    return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
+}
+
+// The cap over a thread's 128 scores, whatever they are.
+__device__ __forceinline__ void cap_scores(const ModParams& m, float (&s)[128]) {
+    if (__any_sync(0xffffffffu, !(row_max_size(s) * m.cap_in <= kCapRange))) {
 #pragma unroll
         for (int e = 0; e < 128; e += 2) {
             const float2 y = cap_any(m, make_float2(s[e], s[e + 1]));
@@ -92,17 +137,20 @@ __device__ __forceinline__ int prefix_of(const ModParams& m, int s, int len, boo
 
 // The KV tiles that a pair of query tiles (2m, 2m+1) visits, in order: step i is KV tile
 // i for i < n_prefix, then lo, lo + 1, ...  A query tile takes part in the steps whose tile
-// lies in its own runs [0, np) and [lo, hi).
+// lies in its own runs [0, np) and [lo, hi): all steps below `steps()` but one run of them.
 struct PairSteps {
     int n_prefix, lo;
     __device__ int tile(int i) const { return i < n_prefix ? i : lo + i - n_prefix; }
 };
 struct TileRuns {
     int np, lo, hi;
-    __device__ bool has(int j) const { return j < np || (j >= lo && j < hi); }
     // one past the last step with work for this tile
     __device__ int steps(const PairSteps& p) const {
         return hi > p.lo ? p.n_prefix + hi - p.lo : max(np, hi);
+    }
+    // the steps below steps() without work are [np, idle_end)
+    __device__ int idle_end(const PairSteps& p) const {
+        return lo <= p.n_prefix ? max(lo, np) : p.n_prefix + max(lo - p.lo, 0);
     }
 };
 __device__ __forceinline__ TileRuns tile_runs(const ModParams& m, int qt, int seg0, int len, int P) {
