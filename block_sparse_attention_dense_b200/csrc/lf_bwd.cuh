@@ -734,8 +734,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         float t0 = 0.f, t1 = 0.f;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            t0 = fmax3(t0, fabsf(__uint_as_float(sa[i])), fabsf(__uint_as_float(sa[i + 1])));
-                            t1 = fmax3(t1, fabsf(__uint_as_float(sb[i])), fabsf(__uint_as_float(sb[i + 1])));
+                            t0 = fmax3_abs(t0, __uint_as_float(sa[i]), __uint_as_float(sa[i + 1]));
+                            t1 = fmax3_abs(t1, __uint_as_float(sb[i]), __uint_as_float(sb[i + 1]));
                         }
                         general = general || __any_sync(0xffffffffu, !(fmaxf(t0, t1) <= prm.mod.fused_max));
                     }

@@ -50,8 +50,6 @@ struct FwdParams {
 struct FwdModParams : FwdParams {
     ModParams mod;
 };
-__device__ __forceinline__ const ModParams* mod_of(const FwdParams&) { return nullptr; }
-__device__ __forceinline__ const ModParams* mod_of(const FwdModParams& p) { return &p.mod; }
 template <int kMod>
 using FwdParamsOf = std::conditional_t<kMod == 0, FwdParams, FwdModParams>;
 
@@ -72,7 +70,123 @@ constexpr int kFwdLaunchRegs = 168;     // 65536 / 384, rounded down to a multip
 constexpr int kFwdCtrlRegs = 64;
 constexpr int kFwdSoftmaxRegs = 216;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a rescale
-constexpr float kFusedSpread = 64.0f;       // log2 of how far below 1 a row's largest P may lie
+constexpr float kBoundedCap = 80.0f;        // cap * log2(e) up to which rows need no maximum
+constexpr float kFusedAbove = 40.0f;        // log2 of the largest P of a fused tile
+
+// One row's softmax numerators over a KV tile whose keys it sees all, under a cap of at most
+// kBoundedCap: P = 2^(C tanh(a s) + bias part) to TMEM over S, an arrival on `half` once its
+// first 64 columns are stored (the caller does the second); returns the row's sum.
+// A row is four chunks of 32 columns.  While chunk c goes through the exp2 unit, chunk c + 1
+// is capped, chunk c - 1 summed and packed, and the range of chunk c + 2 looked at (its vote
+// decides between the narrow fit and the general form two chunks ahead).
+//   dist_bias: bias of column 0; bias2: its step from one column to the next, negated.
+template <bool kBias>
+__device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, float dist_bias, float bias2,
+                                            const float2 (&bias_in8)[4], uint64_t* half) {
+    float sv[128];
+    uint32_t sr[8][16];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tmem_ld16_nowait(t_s + i * 16, sr[i]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tmem_regs_ready(sr[i]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) tmem_ld16_nowait(t_s + i * 16, sr[i]);
+    auto take = [&](int i) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sv[i * 16 + e] = __uint_as_float(sr[i][e]);
+    };
+    auto in_range = [&](int c) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            a = fmax3_abs(a, sv[c * 32 + e], sv[c * 32 + e + 1]);
+            b = fmax3_abs(b, sv[c * 32 + e + 2], sv[c * 32 + e + 3]);
+        }
+        return !__any_sync(0xffffffffu, !(fmaxf(a, b) <= m.fused_max));
+    };
+    // the bias of columns [e, e + 1]: multiples of eight, and within eight
+    auto bias_at = [&](int e) {
+        const float at = fmaf(static_cast<float>(-(e / 8 * 8)), bias2, dist_bias);
+        return f2_add(make_float2(at, at), bias_in8[(e % 8) / 2]);
+    };
+    auto narrow = [&](int e) {
+        const float2 s2 = make_float2(sv[e], sv[e + 1]);
+        const float2 p = cap_fused_factor(m, s2);
+        float2 x;
+        if constexpr (kBias)
+            x = f2_fma(p, s2, bias_at(e));
+        else
+            x = f2_mul(p, s2);
+        sv[e] = x.x;
+        sv[e + 1] = x.y;
+    };
+    auto general = [&](int c) {
+#pragma unroll
+        for (int e = c * 32; e < c * 32 + 32; e += 2) {
+            float2 x = cap_any(m, make_float2(sv[e], sv[e + 1]));
+            if constexpr (kBias) x = f2_add(x, bias_at(e));
+            sv[e] = x.x;
+            sv[e + 1] = x.y;
+        }
+    };
+    take(0);
+    take(1);
+    if (in_range(0)) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) narrow(e);
+    } else {
+        general(0);
+    }
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 2; i < 8; ++i) {
+        tmem_regs_ready(sr[i]);
+        take(i);
+    }
+    bool fits = in_range(1);
+    float p[2][32] = {};
+    float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t pk[16];
+    auto finish = [&](int c, int e) {   // sum and pack columns [e, e + 1] of chunk c
+        const float2 q = make_float2(p[c & 1][e], p[c & 1][e + 1]);
+        rs[(e >> 1) & 1] = f2_add(rs[(e >> 1) & 1], q);
+        pk[e / 2] = pack_bf16(q.x, q.y);
+    };
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        auto exp2_pair = [&](int e) {
+            p[c & 1][e] = fast_exp2(sv[c * 32 + e]);
+            p[c & 1][e + 1] = fast_exp2(sv[c * 32 + e + 1]);
+        };
+        if (c < 3 && fits) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                exp2_pair(e);
+                narrow((c + 1) * 32 + e);
+                if (c > 0) finish(c - 1, e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                exp2_pair(e);
+                if (c > 0) finish(c - 1, e);
+            }
+            if (c < 3) general(c + 1);
+        }
+        if (c < 2) fits = in_range(c + 2);
+        if (c > 0) tmem_st16(t_s + (c - 1) * 16, pk);
+        if (c == 2) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(half);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) finish(3, e);
+    tmem_st16(t_s + 48, pk);
+    return (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+}
 
 template <int D, int kMod>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -125,11 +239,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int m = npairs - 1 - (pg - first_unit_of_segment(seg0, s, 8));   // longest rows first
     if (m < 0) return;
     const bool two = 2 * m + 1 < ntiles;                     // tile 1 exists
-    // KV tiles each query tile needs (under a mask: its steps up to the last one with work)
+    // KV tiles each query tile needs (under a mask: its slots up to the last one with work)
     int nkv0 = prm.causal ? 2 * m + 1 : ntiles;
     int nkv1 = two ? (prm.causal ? 2 * m + 2 : ntiles) : 0;
     int P = 0;                       // prefix length
-    PairSteps steps{};
+    PairSlots slots{};
     TileRuns runs0{}, runs1{};
     if constexpr (kMask) {
         bool bad = false;
@@ -138,13 +252,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         runs0 = tile_runs(prm.mod, 2 * m, seg0, len, P);
         runs1 = two ? tile_runs(prm.mod, 2 * m + 1, seg0, len, P) : TileRuns{0, 0, 0};
         runs1.lo = max(runs1.lo, runs0.lo);   // starts never decrease; all roles rely on it
-        steps.n_prefix = max(runs0.np, runs1.np);
-        steps.lo = max(runs0.lo, steps.n_prefix);
-        nkv0 = runs0.steps(steps);
-        nkv1 = two ? runs1.steps(steps) : 0;
+        slots.n_prefix = max(runs0.np, runs1.np);
+        slots.lo = max(runs0.lo, slots.n_prefix);
+        nkv0 = runs0.slots(slots);
+        nkv1 = two ? runs1.slots(slots) : 0;
     }
     const int nkv = nkv0 > nkv1 ? nkv0 : nkv1;
-    auto kv_tile = [&](int i) { return kMask ? steps.tile(i) : i; };   // of step i
+    // the KV tile of step i: in ascending order, with modified scores in descending order
+    auto kv_tile = [&](int i) { return kMask ? slots.tile(nkv - 1 - i) : kMod ? nkv - 1 - i : i; };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t s_base = smem_addr(smem);
@@ -230,7 +345,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // warp runs this code (one elected lane issues); every wait result is made
             // warp-uniform.  Each commit tracks only the MMAs of the issuing lane.
             const int t = warp - 1;
-            const int nk = t ? nkv1 : nkv0;
+            const int own_slots = t ? nkv1 : nkv0;
+            const int nk = kMod && own_slots > 0 ? nkv : own_slots;   // steps this warp goes through
             if (nk > 0) {
                 constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);
                 constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1);
@@ -256,12 +372,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mma_commit_warp(&bar_s_full[t]);
                     mma_commit_warp(&bar_k_empty[j & 1]);
                 };
-                // work: this tile computes in the current step (always, without a mask); ka
+                // work: this tile computes in the current step (always in the plain kernel); ka
                 // counts those steps, which its own barriers' phases follow, while the K/V
                 // stages' phases follow the step itself
                 const int idle_from = kMask ? (t ? runs1.np : runs0.np) : 0;
-                const int idle_end = kMask ? (t ? runs1.idle_end(steps) : runs0.idle_end(steps)) : 0;
-                auto has_work = [&](int i) { return !kMask || i < idle_from || i >= idle_end; };
+                const int idle_end = kMask ? (t ? runs1.idle_end(slots) : runs0.idle_end(slots)) : 0;
+                auto has_work = [&](int step) {
+                    const int i = nkv - 1 - step;   // the slot
+                    return !kMod || (i < own_slots && (!kMask || i < idle_from || i >= idle_end));
+                };
                 bool work = has_work(0);
                 bool ok = wait(bar_q, 0, 24) && (!work || wait(&bar_k_full[0], 0, 25)) && my_turn();
                 if (ok) {
@@ -275,7 +394,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int j = 0; j < nk && ok; ++j) {
                     const int st = j & 1;
                     const bool next = j + 1 < nk && has_work(j + 1);
-                    if (kMask && !work && !wait(&bar_k_full[st], (j >> 1) & 1, 25)) break;
+                    if (kMod && !work && !wait(&bar_k_full[st], (j >> 1) & 1, 25)) break;
                     if (!wait(&bar_v_full[st], (j >> 1) & 1, 26)) break;
                     if (next && !wait(&bar_k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 28)) break;
                     if (work && !wait(&bar_p_half[t], ka & 1, 18)) break;
@@ -346,17 +465,45 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             bias2 = prm.mod.slopes[h] * -1.4426950408889634f;
             two_sided = !prm.causal || (kMask && P > 0 && !prm.mod.prefix_causal);
         }
+        // Capped scores lie in [-C, C], a bias with slope >= 0 only lowers them, and every row
+        // sees its own key, which has none: the reference 0 will do, without a maximum and
+        // without rescaling.  P then lies below 2^C and the row's sum above 2^-C, both far
+        // inside fp32 and bf16 for C <= kBoundedCap; what falls out below is less than
+        // 2^(C - 126) of the sum
+        bool bounded = false;
+        if constexpr (kCap) bounded = prm.mod.cap_out <= kBoundedCap && (!kBias || bias2 <= 0.f);
+        const float grow = bounded ? INFINITY : kRescaleThreshold;
+        if (bounded) m_ref = 0.f;
         // the bias of the columns within eight, by pairs
         float2 bias_in8[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) bias_in8[i] = make_float2(-bias2 * (2 * i), -bias2 * (2 * i + 1));
         int ka = 0;   // steps with work so far
-        // the tile's KV tiles in order: all of them, or under a mask its two runs
-        for (int j = kMask && runs.np == 0 ? runs.lo : 0; j < (kMask ? max(runs.np, runs.hi) : nk);
-             j = kMask && j + 1 >= runs.np ? max(j + 1, runs.lo) : j + 1) {
+        // the tile's KV tiles: all of them in ascending order; with modified scores in descending
+        // order, under a mask those of its two runs
+        for (int j = !kMod ? 0 : kMask && nk > 0 ? max(runs.np, runs.hi) - 1 : nk - 1; kMod ? j >= 0 : j < nk;
+             j = kMask ? runs.next(j) : kMod ? j - 1 : j + 1) {
             const bool got = mbar_wait_or_abort(&bar_s_full[t], ka & 1, 30, abort_flag);
             if (!__all_sync(0xffffffffu, got)) { failed = true; break; }
             tc_fence_after();
+            const int kv0 = j * 128;
+            const bool diag = !kMask && prm.causal && j == qt;
+            const bool tail = !kMask && kv0 + 128 > len;
+            // every row of the tile sees every key of the step
+            const bool whole = kMask ? kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt) : !(diag || tail);
+            if constexpr (kCap) {
+                if (bounded && whole && !(kBias && two_sided && j >= qt)) {
+                    // a tile under a cap without hidden keys: no maximum, no reference, and so the
+                    // row is taken in chunks of 32 columns as they arrive
+                    l_run += capped_row<kBias>(prm.mod, t_s, static_cast<float>(q_local - kv0) * bias2, bias2, bias_in8,
+                                               &bar_p_half[t]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&bar_p_ready[t]);
+                    ++ka;
+                    continue;
+                }
+            }
             // the row's 128 score columns: eight loads in flight, one wait
             float sv[128];
             {
@@ -371,36 +518,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     for (int e = 0; e < 16; ++e) sv[c * 16 + e] = __uint_as_float(sr[c][e]);
                 }
             }
-            const int kv0 = j * 128;
-            const bool diag = !kMask && prm.causal && j == qt;
-            const bool tail = !kMask && kv0 + 128 > len;
-            // every row of the tile sees every key of the step
-            const bool whole = kMask ? kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt) : !(diag || tail);
-            // fused: the cap and the bias are part of the exponents below, so that they run in
-            // the shadow of the exp2 unit; the maximum of the raw scores, capped, plus the
-            // largest bias bounds the scores from above and serves as the row's maximum.  It
-            // is high by at most the spread between the largest score and the one with the
-            // largest bias (the nearest key), so a tile with a wide spread is not fused
-            bool fused = (kCap || kBias) && whole && !(kBias && two_sided && j >= qt);
-            float mx = 0.f;
-            if constexpr (kCap || kBias) {
-                if (fused) {
-                    mx = row_max(sv);
-                    float near = bias2 <= 0.f ? sv[127] : sv[0];
-                    if constexpr (kCap) {
-                        fused = !__any_sync(0xffffffffu, !(row_max_size(sv) <= prm.mod.fused_max));
-                        mx = cap_fused_one(prm.mod, mx);
-                        if (kBias) near = cap_fused_one(prm.mod, near);
-                    } else {
-                        mx *= prm.scale_log2;
-                        near *= prm.scale_log2;
-                    }
-                    if constexpr (kBias) {
-                        fused = fused && !__any_sync(0xffffffffu, !(mx - near <= kFusedSpread));
-                        mx = fmaf(static_cast<float>(q_local - kv0 - (bias2 <= 0.f ? 127 : 0)), bias2, mx);
-                    }
+            // fused: the bias is part of the exponents below, so that it runs in the shadow of the
+            // exp2 unit.  The maximum of the raw scores plus the largest bias bounds the scores
+            // from above; a tile for which the bound stays near the row's reference (which the
+            // tiles before, nearer ones, have set) needs neither its own maximum nor another
+            // reference: P <= 2^kFusedAbove is as exact as P <= 1
+            bool fused = false;
+            if constexpr (kBias && !kCap) {
+                if (whole && !(two_sided && j >= qt) && ka > 0) {
+                    const float nearest = static_cast<float>(q_local - kv0 - (bias2 <= 0.f ? 127 : 0));
+                    const float bound = fmaf(nearest, bias2, row_max(sv) * prm.scale_log2);
+                    fused = !__any_sync(0xffffffffu, !(bound <= m_ref + kFusedAbove));
                 }
             }
+            float mx = m_ref;
             if (!fused) {
                 // raw scores are scaled in the exponent's FMA; capped ones come scaled
                 const float to_log2 = kCap ? 1.f : prm.scale_log2;
@@ -450,14 +581,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // stale-max rule: keep the old reference unless the row maximum grew a lot
             float alpha = 1.f;
             bool rescale = false;
-            if (ka == 0) {
+            if (ka == 0 && !bounded) {
                 m_ref = mx;
-            } else if (mx > m_ref + kRescaleThreshold) {
+            } else if (mx > m_ref + grow) {
                 alpha = fast_exp2(m_ref - mx);
                 m_ref = mx;
                 rescale = true;
             }
-            if (__any_sync(0xffffffffu, rescale)) {
+            if (!fused && __any_sync(0xffffffffu, rescale)) {
                 // O_t must hold the previous P.V product before it is rescaled (it does: S
                 // of this step completed after it); no P.V of this step has started yet
                 const bool got_o = mbar_wait_or_abort(&bar_o_done[t], (ka - 1) & 1, 31, abort_flag);
@@ -475,8 +606,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // P = 2^(scale * S - m_ref), in four chunks of 32 columns, software-pipelined:
             // the exponentials of chunk c+1 are issued ahead of the row sums, the bf16
             // packing and the TMEM store of chunk c, so that one warp keeps the MUFU busy
-            // (a row that has seen no key yet keeps the reference -inf and gets P = 0)
-            const float neg_m = kMask && m_ref == -INFINITY ? 0.f : -m_ref;
+            const float neg_m = -m_ref;
             // (scale and subtract, and the row sums, in packed pairs)
             const float to_log2 = kCap ? 1.f : prm.scale_log2;
             const float2 sc2 = make_float2(to_log2, to_log2);
@@ -489,11 +619,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     float2 x;
                     if constexpr (decltype(fuse)::value) {
                         float2 off = make_float2(fused_base, fused_base);
-                        if constexpr (kBias) {
+                        {
                             const float at = fmaf(static_cast<float>(-(c * 32 + e) / 8 * 8), bias2, fused_base);
                             off = f2_add(make_float2(at, at), bias_in8[(e % 8) / 2]);
                         }
-                        x = f2_fma(s2, kCap ? cap_fused_factor(*mod_of(prm), s2) : sc2, off);
+                        x = f2_fma(s2, sc2, off);
                     } else {
                         x = f2_fma(s2, sc2, nm2);
                     }
@@ -529,7 +659,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 finish(2, pa);
                 finish(3, pb);
             };
-            if constexpr (kCap || kBias) {
+            if constexpr (kBias && !kCap) {
                 if (fused) probabilities(std::true_type{});
                 else probabilities(std::false_type{});
             } else {

@@ -98,12 +98,18 @@ __device__ __forceinline__ float row_max(const float (&s)[128]) {
     }
     return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
 }
+// max(|a|, |b|, |c|) in one instruction (three-input form).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float row_max_size(const float (&s)[128]) {
     float mq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 128; e += 8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mq[q] = fmax3(mq[q], fabsf(s[e + 2 * q]), fabsf(s[e + 2 * q + 1]));
+        for (int q = 0; q < 4; ++q) mq[q] = fmax3_abs(mq[q], s[e + 2 * q], s[e + 2 * q + 1]);
     }
     return fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
 }
@@ -135,23 +141,27 @@ __device__ __forceinline__ int prefix_of(const ModParams& m, int s, int len, boo
     return min(max(p, 0), len);
 }
 
-// The KV tiles that a pair of query tiles (2m, 2m+1) visits, in order: step i is KV tile
-// i for i < n_prefix, then lo, lo + 1, ...  A query tile takes part in the steps whose tile
-// lies in its own runs [0, np) and [lo, hi): all steps below `steps()` but one run of them.
-struct PairSteps {
+// The KV tiles that a pair of query tiles (2m, 2m+1) needs, in ascending order: slot i is KV
+// tile i for i < n_prefix, then lo, lo + 1, ...  The forward takes the slots from the last to
+// the first: a row then meets its own key, or prefix keys, in its first tile, so that it has
+// a maximum from the start, and with a distance bias close to its last one.  A query tile
+// has work in the slots whose tile lies in its own runs [0, np) and [lo, hi).
+struct PairSlots {
     int n_prefix, lo;
     __device__ int tile(int i) const { return i < n_prefix ? i : lo + i - n_prefix; }
 };
 struct TileRuns {
     int np, lo, hi;
-    // one past the last step with work for this tile
-    __device__ int steps(const PairSteps& p) const {
+    // one past the last slot with work for this tile
+    __device__ int slots(const PairSlots& p) const {
         return hi > p.lo ? p.n_prefix + hi - p.lo : max(np, hi);
     }
-    // the steps below steps() without work are [np, idle_end)
-    __device__ int idle_end(const PairSteps& p) const {
+    // the slots below slots() without work are [np, idle_end)
+    __device__ int idle_end(const PairSlots& p) const {
         return lo <= p.n_prefix ? max(lo, np) : p.n_prefix + max(lo - p.lo, 0);
     }
+    // the tile after j, in the forward's order (below 0: none)
+    __device__ int next(int j) const { return j - 1 < lo && j - 1 >= np ? np - 1 : j - 1; }
 };
 __device__ __forceinline__ TileRuns tile_runs(const ModParams& m, int qt, int seg0, int len, int P) {
     const int q0 = qt * 128;

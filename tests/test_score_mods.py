@@ -284,10 +284,17 @@ def test_a_mask_that_hides_nothing_is_the_plain_attention():
     desc = c.desc(g)
     p = lf.Buffers(desc)
     lf.lazyflash_step(desc, g["q"], g["k"], g["v"], g["dout"], 0.0, 3, 0, p)
-    assert torch.equal(b.o, p.o) and torch.equal(b.lse, p.lse)
+    # the same scores, but the tiles in another order: the row's reference m differs, and with
+    # it where bf16 rounds each P (b of each term on either side: twice O's tolerance); in the
+    # row's sum of n <= 300 positive terms, kept in fp32, each addition, each exp2 (4 u) and
+    # each exponent (60 u of 1, |z - m| < 60) is off by as much on either side
+    tol = reference(c, m)[1]
+    assert ((b.o.double() - p.o.double()).abs().cpu() <= 2 * tol["o"]).all()
+    assert ((b.lse - p.lse).abs() <= 2 * (300 + 64) * U + 8 * U * p.lse.abs()).all()
     for x in ("dq", "dk", "dv"):   # dQ is summed by atomics, in any order
-        a, z = getattr(b, x).float(), getattr(p, x).float()
-        assert (a - z).norm() <= 2 * B * z.norm()
+        # dS and P of the backward come from LSE and D; D from O (see the tolerances above)
+        a, z = getattr(b, x).double().cpu(), getattr(p, x).double().cpu()
+        assert ((a - z).abs() <= 2 * reference(c, m, b.w.cpu())[1][x]).all()
 
 
 @gpu
