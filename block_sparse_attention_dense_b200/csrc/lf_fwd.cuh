@@ -73,16 +73,26 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a re
 constexpr float kBoundedCap = 80.0f;        // cap * log2(e) up to which rows need no maximum
 constexpr float kFusedAbove = 40.0f;        // log2 of the largest P of a fused tile
 
-// One row's softmax numerators over a KV tile whose keys it sees all, under a cap of at most
-// kBoundedCap: P = 2^(C tanh(a s) + bias part) to TMEM over S, an arrival on `half` once its
+// The keys of a KV tile that a row sees, counted from the tile's first: [0, pre) and the
+// own + 1 keys from `first` on (one unsigned compare for those: with two, the compiler
+// spilled a quarter of the scores).
+struct RowView {
+    int pre, first;
+    unsigned own;
+    __device__ bool sees(int e) const { return e < pre || static_cast<unsigned>(e - first) <= own; }
+};
+
+// One row's softmax numerators over a KV tile, under a cap of at most kBoundedCap: P = 2^(C tanh(a s) + bias part) to TMEM over S, an arrival on `half` once its
 // first 64 columns are stored (the caller does the second); returns the row's sum.
 // A row is four chunks of 32 columns.  While chunk c goes through the exp2 unit, chunk c + 1
 // is capped, chunk c - 1 summed and packed, and the range of chunk c + 2 looked at (its vote
 // decides between the narrow fit and the general form two chunks ahead).
-//   dist_bias: bias of column 0; bias2: its step from one column to the next, negated.
-template <bool kBias>
+//   dist_bias: bias of column 0; bias2: its step from one column to the next, negated;
+//   kHidden: the tile has keys that some row does not see (view: this row's).  A variant of
+//   its own: a branch per chunk split the pairing above and cost 10 % on whole tiles.
+template <bool kBias, bool kHidden>
 __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, float dist_bias, float bias2,
-                                            const float2 (&bias_in8)[4], uint64_t* half) {
+                                            const float2 (&bias_in8)[4], const RowView& view, uint64_t* half) {
     float sv[128];
     uint32_t sr[8][16];
 #pragma unroll
@@ -130,6 +140,10 @@ __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, fl
             sv[e + 1] = x.y;
         }
     };
+    auto hide = [&](int c) {
+#pragma unroll
+        for (int e = c * 32; e < c * 32 + 32; ++e) sv[e] = view.sees(e) ? sv[e] : -INFINITY;
+    };
     take(0);
     take(1);
     if (in_range(0)) {
@@ -138,6 +152,7 @@ __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, fl
     } else {
         general(0);
     }
+    if (kHidden) hide(0);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 2; i < 8; ++i) {
@@ -174,6 +189,7 @@ __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, fl
             }
             if (c < 3) general(c + 1);
         }
+        if (c < 3 && kHidden) hide(c + 1);
         if (c < 2) fits = in_range(c + 2);
         if (c > 0) tmem_st16(t_s + (c - 1) * 16, pk);
         if (c == 2) {
@@ -491,12 +507,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const bool tail = !kMask && kv0 + 128 > len;
             // every row of the tile sees every key of the step
             const bool whole = kMask ? kv0 + 128 <= all_prefix || (kv0 >= all_from && j < qt) : !(diag || tail);
+            // the row's visible keys of the tile (a padding row takes the last row's)
+            RowView view{0, -kv0, static_cast<unsigned>(len - 1)};
+            if constexpr (kMask) {
+                const int row = min(q_local, len - 1);
+                view.pre = (prm.mod.prefix_causal ? min(P_row, row + 1) : P_row) - kv0;
+                view.first = from - kv0;
+                view.own = row - from;
+            } else if (diag) {
+                view.own = min(q_local, len - 1);
+            }
             if constexpr (kCap) {
-                if (bounded && whole && !(kBias && two_sided && j >= qt)) {
-                    // a tile under a cap without hidden keys: no maximum, no reference, and so the
-                    // row is taken in chunks of 32 columns as they arrive
-                    l_run += capped_row<kBias>(prm.mod, t_s, static_cast<float>(q_local - kv0) * bias2, bias2, bias_in8,
-                                               &bar_p_half[t]);
+                if (bounded && !(kBias && two_sided && j >= qt)) {
+                    // a tile under a cap: no maximum, no reference, and so the row is taken in
+                    // chunks of 32 columns as they arrive
+                    const float dist_bias = static_cast<float>(q_local - kv0) * bias2;
+                    l_run += whole ? capped_row<kBias, false>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t])
+                                   : capped_row<kBias, true>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t]);
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(&bar_p_ready[t]);
@@ -553,18 +580,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         }
                     }
                 }
-                if constexpr (kMask) {
+                if constexpr (kMod != 0) {
                     if (!whole) {
-                        // visible: [0, pre) and [from, to] (a padding row takes the last row's)
-                        const int row = min(q_local, len - 1);
-                        const int pre = (prm.mod.prefix_causal ? min(P_row, row + 1) : P_row) - kv0;
-                        const int first = from - kv0;
-                        const unsigned own = row - from;
-                        // (one unsigned compare for [from, to]: with two, the compiler spilled
-                        // a quarter of the scores)
 #pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            sv[e] = (e < pre || static_cast<unsigned>(e - first) <= own) ? sv[e] : -INFINITY;
+                        for (int e = 0; e < 128; ++e) sv[e] = view.sees(e) ? sv[e] : -INFINITY;
                     }
                 } else if (diag || tail) {
 #pragma unroll
