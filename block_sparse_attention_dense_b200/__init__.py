@@ -114,9 +114,9 @@ def _load():
     L.lf_sync_status.argtypes = [vp]
     L.lf_sync_status.restype = i32
     mptr = ctypes.POINTER(lf_score_mod)
-    L.lf_attn_fwd_mod.argtypes = [dptr, mptr, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.lf_attn_fwd_mod.argtypes = [dptr, mptr] + [vp] * 7
     L.lf_attn_fwd_mod.restype = i32
-    L.lf_attn_bwd_mod.argtypes = [dptr, mptr] + [vp] * 14 + [sz, vp]
+    L.lf_attn_bwd_mod.argtypes = [dptr, mptr] + [vp] * 15 + [sz, vp]
     L.lf_attn_bwd_mod.restype = i32
     i64, qptr = ctypes.c_int64, ctypes.POINTER(lf_qk_desc)
     L.lf_qk_norm_rope.argtypes = [qptr] + [vp, i64] * 4 + [vp]
@@ -347,28 +347,29 @@ def _check_attention(desc, mod, q, k, v, rest=()):
     return dev
 
 
-def lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, ws=None, stream=None):
+def lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, o_low=None, stream=None):
     dev = _check_attention(desc, mod, q, k, v, [
-        ("o", o, desc.hq), ("lse", lse, (torch.float32, desc.hq * desc.total_tokens))])
+        ("o", o, desc.hq), ("o_low", o_low, desc.hq),
+        ("lse", lse, (torch.float32, desc.hq * desc.total_tokens))])
     L = _load()
-    args = [t.data_ptr() for t in (q, k, v, o, lse)] + [_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()]
+    args = [None if t is None else t.data_ptr() for t in (q, k, v, o, o_low, lse)]
     _check(_on_device(dev, lambda s: L.lf_attn_fwd_mod(ctypes.byref(desc), ctypes.byref(mod), *args, s), stream),
            "lf_attn_fwd_mod")
 
 
 def lf_attn_bwd_mod(desc, mod, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv,
-                    ws, stream=None):
+                    ws, o_low=None, stream=None):
     rows = (torch.float32, desc.hq * desc.total_tokens)
     heads = desc.nseq * desc.hq
     nb = heads * ((desc.max_seqlen + desc.block_q - 1) // desc.block_q)
     dev = _check_attention(desc, mod, q, k, v, [
-        ("o", o, desc.hq), ("lse", lse, rows), ("dout", dout, desc.hq), ("D", D, rows),
+        ("o", o, desc.hq), ("o_low", o_low, desc.hq), ("lse", lse, rows), ("dout", dout, desc.hq), ("D", D, rows),
         ("block_weight", block_weight, (torch.float32, nb)), ("kept_idx", kept_idx, (torch.int32, nb)),
         ("kept_cnt", kept_cnt, (torch.int32, heads)), ("dq", dq, desc.hq), ("dk", dk, desc.hkv),
         ("dv", dv, desc.hkv)])
     L = _load()
     args = [None if t is None else t.data_ptr()
-            for t in (q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv, ws)]
+            for t in (q, k, v, o, o_low, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv, ws)]
     args.append(0 if ws is None else ws.numel() * ws.element_size())
     _check(_on_device(dev, lambda s: L.lf_attn_bwd_mod(ctypes.byref(desc), ctypes.byref(mod), *args, s), stream),
            "lf_attn_bwd_mod")

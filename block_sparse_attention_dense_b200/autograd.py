@@ -39,12 +39,16 @@ class LazyFlashAttention(torch.autograd.Function):
         desc = make_desc(cu_seqlens, max_seqlen, T, hq, hkv, d, scale, causal, block_q)
         o = torch.empty_like(q)
         lse = torch.empty(hq, T, dtype=torch.float32, device=q.device)
+        o_low = None
         if mod is None:
             lf_attn_fwd(desc, q, k, v, o, lse)
         else:
-            lf_attn_fwd_mod(desc, mod, q, k, v, o, lse)
+            # O's rounding residual, kept for the backward's D (not when no gradient is asked for)
+            if any(ctx.needs_input_grad):
+                o_low = torch.empty_like(q)
+            lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, o_low)
         ctx.mod = mod
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low)
         ctx.desc = desc
         ctx.delta = float(delta)
         ctx.seed = int(seed)
@@ -54,19 +58,21 @@ class LazyFlashAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_o):
-        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        q, k, v, o, lse, cu_seqlens, o_low = ctx.saved_tensors
         desc = ctx.desc
         dout = grad_o.to(torch.bfloat16).contiguous()
         # the backward's own buffers only: o and lse are the forward's saved tensors
         bufs = Buffers(desc, device=q.device, forward=False)
-        lf_block_select(desc, dout, o, ctx.delta, ctx.seed, ctx.step, 0, bufs.norm, bufs.D,
+        # with modified scores the backward computes D itself, from o and its residual
+        D = bufs.D if ctx.mod is None else None
+        lf_block_select(desc, dout, o, ctx.delta, ctx.seed, ctx.step, 0, bufs.norm, D,
                         bufs.tau, bufs.w, bufs.keep, bufs.kept_idx, bufs.kept_cnt)
-        args = (q, k, v, o, lse, dout, bufs.D, bufs.w, bufs.kept_idx, bufs.kept_cnt, bufs.dq, bufs.dk,
+        args = (q, k, v, o, lse, dout, D, bufs.w, bufs.kept_idx, bufs.kept_cnt, bufs.dq, bufs.dk,
                 bufs.dv, bufs.ws)
         if ctx.mod is None:
             lf_attn_bwd(desc, *args)
         else:
-            lf_attn_bwd_mod(desc, ctx.mod, *args)
+            lf_attn_bwd_mod(desc, ctx.mod, *args, o_low)
         if ctx.selection_out is not None:
             ctx.selection_out.update(norm=bufs.norm, tau=bufs.tau, keep=bufs.keep,
                                      weight=bufs.w, kept_cnt=bufs.kept_cnt, step=ctx.step)

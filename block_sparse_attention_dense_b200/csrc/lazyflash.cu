@@ -162,7 +162,7 @@ lf::ModParams mod_params(const lf_attn_desc* d, const lf_score_mod* m) {
 
 template <int D, int kMod>
 lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void* q, const void* k,
-                     const void* v, void* o, float* lse, cudaStream_t st) {
+                     const void* v, void* o, void* o_low, float* lse, cudaStream_t st) {
     CUtensorMap mq, mk, mv;
     if (!make_thd_map(&mq, q, d->total_tokens, d->hq, D) ||
         !make_thd_map(&mk, k, d->total_tokens, d->hkv, D) ||
@@ -179,7 +179,10 @@ lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void*
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    if constexpr (kMod != 0) p.mod = mod_params(d, mod);
+    if constexpr (kMod != 0) {
+        p.mod = mod_params(d, mod);
+        p.o_low = static_cast<__nv_bfloat16*>(o_low);
+    }
     const uint32_t smem = lf::FwdSmem<D>::kAlloc;
     if (cudaFuncSetAttribute(lf::attn_fwd_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
@@ -225,8 +228,8 @@ lf_status launch_norms(const lf_attn_desc* d, const void* dout, const void* o, f
 // the workspace when the caller passed none), attn_bwd_kernel, dQ conversion.
 // key_last: scratch of a modifier with row_start.
 template <int D, int kMod>
-lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* q,
-                     const void* k, const void* v, const void* o, const float* lse, const void* dout, const float* Dgiven,
+lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* o_low,
+                     const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout, const float* Dgiven,
                      const float* w, const int32_t* kidx, const int32_t* kcnt, void* dq, void* dk,
                      void* dv, void* ws, cudaStream_t st) {
     // Q and dO also in 64-row boxes: a query tile with one live half loads only that half
@@ -268,10 +271,10 @@ lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* ke
     }
     const dim3 blocks(nbmax_of(d), d->hq, d->nseq);
     float* Dw = Dgiven ? nullptr : reinterpret_cast<float*>(base + bwd_ws_layout(d, true).D);
-    lf::bwd_prologue_kernel<D><<<blocks, lf::kNormThreads, 0, st>>>(
+    lf::bwd_prologue_kernel<D, kMod != 0><<<blocks, lf::kNormThreads, 0, st>>>(
         d->cu_seqlens, d->total_tokens, d->max_seqlen, d->hq, d->block_q, nbmax_of(d), w, dq_acc,
         static_cast<const __nv_bfloat16*>(dout), static_cast<const __nv_bfloat16*>(o), Dw,
-        mod ? mod->row_start : nullptr, key_last);
+        static_cast<const __nv_bfloat16*>(o_low), mod ? mod->row_start : nullptr, key_last);
     if (launch_status() != LF_OK) return LF_ERR_CUDA;
     const float* Dv = Dgiven ? Dgiven : Dw;
     lf::BwdParamsOf<kMod> p{};
@@ -348,18 +351,18 @@ lf_status by_variant(const lf_attn_desc* d, const lf_score_mod* mod, F&& f) {
     }
 }
 lf_status launch_fwd_any(const lf_attn_desc* d, const lf_score_mod* mod, const void* q, const void* k,
-                         const void* v, void* o, float* lse, cudaStream_t st) {
+                         const void* v, void* o, void* o_low, float* lse, cudaStream_t st) {
     return by_variant(d, mod, [&](auto D, auto M) {
-        return launch_fwd<decltype(D)::value, decltype(M)::value>(d, mod, q, k, v, o, lse, st);
+        return launch_fwd<decltype(D)::value, decltype(M)::value>(d, mod, q, k, v, o, o_low, lse, st);
     });
 }
-lf_status launch_bwd_any(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* q,
-                         const void* k, const void* v, const void* o, const float* lse, const void* dout,
+lf_status launch_bwd_any(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* key_last, const void* o_low,
+                         const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                          const float* Dgiven, const float* w, const int32_t* kidx, const int32_t* kcnt, void* dq,
                          void* dk, void* dv, void* ws, cudaStream_t st) {
     return by_variant(d, mod, [&](auto D, auto M) {
-        return launch_bwd<decltype(D)::value, decltype(M)::value>(d, mod, key_last, q, k, v, o, lse, dout, Dgiven,
-                                                                  w, kidx, kcnt, dq, dk, dv, ws, st);
+        return launch_bwd<decltype(D)::value, decltype(M)::value>(d, mod, key_last, o_low, q, k, v, o, lse, dout,
+                                                                  Dgiven, w, kidx, kcnt, dq, dk, dv, ws, st);
     });
 }
 
@@ -580,7 +583,8 @@ lf_status lf_workspace_size(const lf_attn_desc* desc, int which, size_t* bytes) 
 }
 
 static lf_status attn_fwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                               const void* k, const void* v, void* o, float* lse, lf_stream_t stream) {
+                               const void* k, const void* v, void* o, void* o_low, float* lse,
+                               lf_stream_t stream) {
     lf_status st = check_desc(desc);
     if (st != LF_OK) return st;
     if (!q || !k || !v || !o || !lse) return LF_ERR_INVALID_ARG;
@@ -590,24 +594,23 @@ static lf_status attn_fwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod
     if (desc->total_tokens == 0 || desc->max_seqlen == 0) return LF_OK;
     if ((st = prepare_device()) != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return mirror_after(launch_fwd_any(desc, mod, q, k, v, o, lse, s), s);
+    return mirror_after(launch_fwd_any(desc, mod, q, k, v, o, o_low, lse, s), s);
 }
 
 lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,
                       void* o, float* lse, void* ws, size_t ws_bytes, lf_stream_t stream) {
     (void)ws;
     (void)ws_bytes;
-    return attn_fwd_impl(desc, nullptr, q, k, v, o, lse, stream);
+    return attn_fwd_impl(desc, nullptr, q, k, v, o, nullptr, lse, stream);
 }
 
 lf_status lf_attn_fwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                          const void* k, const void* v, void* o, float* lse, void* ws,
-                          size_t ws_bytes, lf_stream_t stream) {
-    (void)ws;
-    (void)ws_bytes;
+                          const void* k, const void* v, void* o, void* o_low, float* lse,
+                          lf_stream_t stream) {
     lf_status st = check_desc(desc);
     if (st == LF_OK) st = check_mod(desc, mod);
-    return st != LF_OK ? st : attn_fwd_impl(desc, mod, q, k, v, o, lse, stream);
+    if (st == LF_OK && !aligned16(o_low)) st = LF_ERR_INVALID_ARG;
+    return st != LF_OK ? st : attn_fwd_impl(desc, mod, q, k, v, o, o_low, lse, stream);
 }
 
 static lf_status block_select_impl(const lf_attn_desc* desc, const void* dout, const void* o,
@@ -682,7 +685,7 @@ lf_status lf_block_select_rule(const lf_attn_desc* desc, const void* dout, const
 }
 
 static lf_status attn_bwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                               const void* k, const void* v, const void* o, const float* lse,
+                               const void* k, const void* v, const void* o, const void* o_low, const float* lse,
                                const void* dout, const float* D, const float* block_weight,
                                const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
                                void* dv, void* ws, size_t ws_bytes, lf_stream_t stream) {
@@ -705,7 +708,7 @@ static lf_status attn_bwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod
         starts ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + key_last_offset(desc)) : nullptr;
     if ((st = prepare_device()) != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return mirror_after(launch_bwd_any(desc, mod, key_last, q, k, v, o, lse, dout, D, block_weight, kept_idx,
+    return mirror_after(launch_bwd_any(desc, mod, key_last, o_low, q, k, v, o, lse, dout, D, block_weight, kept_idx,
                                        kept_cnt, dq, dk, dv, ws, s),
                         s);
 }
@@ -715,19 +718,20 @@ lf_status lf_attn_bwd(const lf_attn_desc* desc, const void* q, const void* k, co
                       const float* block_weight, const int32_t* kept_idx,
                       const int32_t* kept_cnt, void* dq, void* dk, void* dv, void* ws,
                       size_t ws_bytes, lf_stream_t stream) {
-    return attn_bwd_impl(desc, nullptr, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv,
+    return attn_bwd_impl(desc, nullptr, q, k, v, o, nullptr, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv,
                          ws, ws_bytes, stream);
 }
 
 lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                          const void* k, const void* v, const void* o, const float* lse,
-                          const void* dout, const float* D, const float* block_weight,
+                          const void* k, const void* v, const void* o, const void* o_low,
+                          const float* lse, const void* dout, const float* D, const float* block_weight,
                           const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
                           void* dv, void* ws, size_t ws_bytes, lf_stream_t stream) {
     lf_status st = check_desc(desc);
     if (st == LF_OK) st = check_mod(desc, mod);
+    if (st == LF_OK && (!aligned16(o_low) || (o_low && D))) st = LF_ERR_INVALID_ARG;
     return st != LF_OK ? st
-                       : attn_bwd_impl(desc, mod, q, k, v, o, lse, dout, D, block_weight, kept_idx, kept_cnt, dq,
+                       : attn_bwd_impl(desc, mod, q, k, v, o, o_low, lse, dout, D, block_weight, kept_idx, kept_cnt, dq,
                                        dk, dv, ws, ws_bytes, stream);
 }
 
@@ -756,7 +760,7 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
     if (st != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // launch_bwd clears the accumulators it uses before the kernel
-    return mirror_after(launch_bwd_any(desc, nullptr, nullptr, q, k, v, o, lse, dout, D, block_weight, kept_idx,
+    return mirror_after(launch_bwd_any(desc, nullptr, nullptr, nullptr, q, k, v, o, lse, dout, D, block_weight, kept_idx,
                                        kept_cnt, dq, dk, dv, ws, s),
                         s);
 }

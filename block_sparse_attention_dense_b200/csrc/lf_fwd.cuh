@@ -49,6 +49,7 @@ struct FwdParams {
 };
 struct FwdModParams : FwdParams {
     ModParams mod;
+    __nv_bfloat16* o_low;      // [T][hq][D] what rounding took from o, or null
 };
 template <int kMod>
 using FwdParamsOf = std::conditional_t<kMod == 0, FwdParams, FwdModParams>;
@@ -73,6 +74,18 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 of the largest P before a re
 constexpr float kBoundedCap = 80.0f;        // cap * log2(e) up to which rows need no maximum
 constexpr float kFusedAbove = 40.0f;        // log2 of the largest P of a fused tile
 
+// Adds a packed bf16 pair to a pair of fp32 sums.
+__device__ __forceinline__ void add_packed(float2& sum, uint32_t packed) {
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; add.f32.bf16 %0, l, %0; add.f32.bf16 %1, h, %1;}"
+        : "+f"(sum.x), "+f"(sum.y)
+        : "r"(packed));
+}
+
+// A row's sum of P, as computed and as rounded to bf16.
+struct RowSums {
+    float exact, rounded;
+};
+
 // The keys of a KV tile that a row sees, counted from the tile's first: [0, pre) and the
 // own + 1 keys from `first` on (one unsigned compare for those: with two, the compiler
 // spilled a quarter of the scores).
@@ -83,7 +96,7 @@ struct RowView {
 };
 
 // One row's softmax numerators over a KV tile, under a cap of at most kBoundedCap: P = 2^(C tanh(a s) + bias part) to TMEM over S, an arrival on `half` once its
-// first 64 columns are stored (the caller does the second); returns the row's sum.
+// first 64 columns are stored (the caller does the second); returns the row's sums.
 // A row is four chunks of 32 columns.  While chunk c goes through the exp2 unit, chunk c + 1
 // is capped, chunk c - 1 summed and packed, and the range of chunk c + 2 looked at (its vote
 // decides between the narrow fit and the general form two chunks ahead).
@@ -91,7 +104,7 @@ struct RowView {
 //   kHidden: the tile has keys that some row does not see (view: this row's).  A variant of
 //   its own: a branch per chunk split the pairing above and cost 10 % on whole tiles.
 template <bool kBias, bool kHidden>
-__device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, float dist_bias, float bias2,
+__device__ __forceinline__ RowSums capped_row(const ModParams& m, uint32_t t_s, float dist_bias, float bias2,
                                             const float2 (&bias_in8)[4], const RowView& view, uint64_t* half) {
     float sv[128];
     uint32_t sr[8][16];
@@ -161,12 +174,13 @@ __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, fl
     }
     bool fits = in_range(1);
     float p[2][32] = {};
-    float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, rounded[2] = {rs[0], rs[0]};
     uint32_t pk[16];
     auto finish = [&](int c, int e) {   // sum and pack columns [e, e + 1] of chunk c
         const float2 q = make_float2(p[c & 1][e], p[c & 1][e + 1]);
         rs[(e >> 1) & 1] = f2_add(rs[(e >> 1) & 1], q);
         pk[e / 2] = pack_bf16(q.x, q.y);
+        add_packed(rounded[(e >> 1) & 1], pk[e / 2]);
     };
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -201,7 +215,8 @@ __device__ __forceinline__ float capped_row(const ModParams& m, uint32_t t_s, fl
 #pragma unroll
     for (int e = 0; e < 32; e += 2) finish(3, e);
     tmem_st16(t_s + 48, pk);
-    return (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+    return {(rs[0].x + rs[0].y) + (rs[1].x + rs[1].y),
+            (rounded[0].x + rounded[0].y) + (rounded[1].x + rounded[1].y)};
 }
 
 template <int D, int kMod>
@@ -456,6 +471,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int qt = 2 * m + t;
         const int q_local = qt * 128 + r;
         float m_ref = -INFINITY, l_run = 0.f;
+        // kMod: the sum of P as rounded, which O is divided by.  P V with the rounded P over their
+        // own sum is an average of V again, exactly V for a row that lies on one key; over the
+        // exact sum it is off by that key's rounding, and so is D = <dO, O>, while dS = P (dP - D)
+        // cancels: such rows got gradients as large as the rounding instead of none
+        [[maybe_unused]] float l_rounded = 0.f;
         bool failed = false;
         int P_row = 0, from = 0;      // kMask: the prefix length, the row's first own key
         int all_prefix = 0, all_from = 0;   // keys that every row of the tile sees: below
@@ -522,8 +542,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     // a tile under a cap: no maximum, no reference, and so the row is taken in
                     // chunks of 32 columns as they arrive
                     const float dist_bias = static_cast<float>(q_local - kv0) * bias2;
-                    l_run += whole ? capped_row<kBias, false>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t])
-                                   : capped_row<kBias, true>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t]);
+                    const RowSums sums =
+                        whole ? capped_row<kBias, false>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t])
+                              : capped_row<kBias, true>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t]);
+                    l_run += sums.exact;
+                    l_rounded += sums.rounded;
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(&bar_p_ready[t]);
@@ -651,6 +674,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             };
             float2 rsA = make_float2(0.f, 0.f), rsB = make_float2(0.f, 0.f);
+            [[maybe_unused]] float2 roundedA = rsA, roundedB = rsA;
             auto finish = [&](int c, const float (&p)[32]) {
                 uint32_t pk[16];
 #pragma unroll
@@ -660,6 +684,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     else
                         rsA = f2_add(rsA, make_float2(p[2 * e], p[2 * e + 1]));
                     pk[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+                    if constexpr (kMod != 0) add_packed((e & 1) ? roundedB : roundedA, pk[e]);
                 }
                 tmem_st16(t_s + c * 16, pk);   // P (packed) over S columns already read
             };
@@ -686,6 +711,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             const float rs_all = (rsA.x + rsA.y) + (rsB.x + rsB.y);
             l_run = l_run * alpha + rs_all;
+            if constexpr (kMod != 0)
+                l_rounded = l_rounded * alpha + ((roundedA.x + roundedA.y) + (roundedB.x + roundedB.y));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar_p_ready[t]);
@@ -698,7 +725,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (have) {
             tc_fence_after();
             const bool row_ok = q_local < len;
-            const float inv_l = 1.f / l_run;
+            const float inv_l = 1.f / (kMod ? l_rounded : l_run);
             const int tok = seg0 + q_local;
             __nv_bfloat16* orow = prm.o + ((size_t)tok * prm.hq + h) * D;
 #pragma unroll
@@ -714,6 +741,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         pk.z = pack_bf16(ov[e8 * 8 + 4] * inv_l, ov[e8 * 8 + 5] * inv_l);
                         pk.w = pack_bf16(ov[e8 * 8 + 6] * inv_l, ov[e8 * 8 + 7] * inv_l);
                         *reinterpret_cast<uint4*>(orow + c * 32 + e8 * 8) = pk;
+                        if constexpr (kMod != 0) {
+                            if (prm.o_low) {
+                                const uint32_t hi[4] = {pk.x, pk.y, pk.z, pk.w};
+                                uint32_t low[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    low[i] = pack_bf16(fmaf(ov[e8 * 8 + 2 * i], inv_l, -__uint_as_float(hi[i] << 16)),
+                                                       fmaf(ov[e8 * 8 + 2 * i + 1], inv_l,
+                                                            -__uint_as_float(hi[i] & 0xffff0000u)));
+                                *reinterpret_cast<uint4*>(prm.o_low + (orow - prm.o) + c * 32 + e8 * 8) =
+                                    make_uint4(low[0], low[1], low[2], low[3]);
+                            }
+                        }
                     }
                 }
             }

@@ -47,12 +47,14 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
 }
 
 // Rows [r0, r1) of head h: returns this thread's sum of squares of dO; writes
-// D[h][t] = <dO_t, O_t> when Dout is given.  Every thread of the CTA calls it.
-template <int D>
+// D[h][t] = <dO_t, O_t> when Dout is given (kLow: <dO_t, O_t + o_low_t>).  Every thread of
+// the CTA calls it.
+template <int D, bool kLow = false>
 __device__ __forceinline__ float block_rows_pass(int r0, int r1, int h, int hq, int T,
                                                  const __nv_bfloat16* __restrict__ dout,
                                                  const __nv_bfloat16* __restrict__ o,
-                                                 float* __restrict__ Dout) {
+                                                 float* __restrict__ Dout,
+                                                 const __nv_bfloat16* __restrict__ o_low = nullptr) {
     constexpr int LPR = D / 8;                  // lanes per row
     constexpr int RPW = 32 / LPR;               // rows per warp instruction
     constexpr int STEP = (kNormThreads / 32) * RPW;
@@ -61,15 +63,17 @@ __device__ __forceinline__ float block_rows_pass(int r0, int r1, int h, int hq, 
     const int sub = lane / LPR, c8 = (lane % LPR) * 8;
     float ss = 0.f;
     for (int t0 = r0 + warp * RPW + sub; t0 < r1 + sub; t0 += STEP * U) {
-        uint4 a[U], b[U];
+        uint4 a[U], b[U], low[kLow ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = t0 + u * STEP;
             a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (kLow) low[u] = make_uint4(0u, 0u, 0u, 0u);
             if (t < r1) {
                 const size_t off = ((size_t)t * hq + h) * D + c8;
                 a[u] = ld_stream16(dout + off);
                 if (Dout) b[u] = ld_stream16(o + off);
+                if (kLow) low[u] = ld_stream16(o_low + off);
             }
         }
 #pragma unroll
@@ -77,6 +81,7 @@ __device__ __forceinline__ float block_rows_pass(int r0, int r1, int h, int hq, 
             ss += bf16x8_dot<D>(a[u], a[u]);
             if (Dout) {
                 float dot = bf16x8_dot<D>(a[u], b[u]);
+                if (kLow) dot += bf16x8_dot<D>(a[u], low[u]);
 #pragma unroll
                 for (int off = LPR / 2; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
                 const int t = t0 + u * STEP;
@@ -464,16 +469,17 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float4* __restric
 // Prologue: zero the kept blocks' accumulator rows and, when Dw is given (the caller
 // passed no D), compute D = <dO_t, O_t> for the kept blocks' rows and write 0 for the
 // dropped blocks' rows (the backward reads them, with weight 0, when a 128-row tile
-// holds one kept and one dropped 64-row block).  With key_last (modified scores with
+// holds one kept and one dropped 64-row block).  kMod (modified scores): with o_low, O's
+// rounding residual from the forward, D is that of the unrounded O; with key_last (
 // per-row starts) the head-0 CTAs also find, for each of the block's keys, the last row of
 // the segment that sees it: one bisection per key, here rather than in the backward's CTAs,
 // each of which would repeat it for every head group.
-template <int D>
+template <int D, bool kMod>
 __global__ void __launch_bounds__(kNormThreads) bwd_prologue_kernel(
     const int32_t* __restrict__ cu_seqlens, int T, int max_seqlen, int H, int block_q, int nbmax,
     const float* __restrict__ w, float* __restrict__ acc, const __nv_bfloat16* __restrict__ dout,
-    const __nv_bfloat16* __restrict__ o, float* __restrict__ Dw, const int32_t* __restrict__ row_start,
-    int32_t* __restrict__ key_last) {
+    const __nv_bfloat16* __restrict__ o, float* __restrict__ Dw, const __nv_bfloat16* __restrict__ o_low,
+    const int32_t* __restrict__ row_start, int32_t* __restrict__ key_last) {
     const int b = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
     int seg0, len;
     if (!load_segment(cu_seqlens, s, T, max_seqlen, seg0, len, 50)) return;
@@ -485,13 +491,16 @@ __global__ void __launch_bounds__(kNormThreads) bwd_prologue_kernel(
         const int n4 = (r1 - r0) * D / 4;
         for (int i = threadIdx.x; i < n4; i += blockDim.x) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (key_last && h == 0) {
+    if (kMod && key_last && h == 0) {
         for (int u = r0 + threadIdx.x; u < r1; u += blockDim.x)
             key_last[seg0 + u] = last_row_of_key(row_start, seg0, len, u);
     }
     if (Dw) {
         if (kept) {
-            (void)block_rows_pass<D>(seg0 + r0, seg0 + r1, h, H, T, dout, o, Dw);
+            if (kMod && o_low)
+                (void)block_rows_pass<D, true>(seg0 + r0, seg0 + r1, h, H, T, dout, o, Dw, o_low);
+            else
+                (void)block_rows_pass<D>(seg0 + r0, seg0 + r1, h, H, T, dout, o, Dw);
         } else {
             for (int t = seg0 + r0 + threadIdx.x; t < seg0 + r1; t += blockDim.x) Dw[(size_t)h * T + t] = 0.f;
         }

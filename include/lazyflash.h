@@ -249,21 +249,29 @@ typedef struct {
 } lf_score_mod;
 
 /* lf_attn_fwd and lf_attn_bwd with modified scores.  Arguments, results, workspace
- * (lf_workspace_size) and errors are theirs; the selection between the two is
- * lf_block_select's.  prefix_len and row_start need causal = 1 (LF_ERR_UNSUPPORTED
- * otherwise).  Device arrays of the modifier need only their type's alignment; their contents are
- * checked on the device by the forward (a negative prefix by both): one that breaks its
- * rule is reported by the next call (LF_ERR_INVALID_ARG), with the results undefined.
- * Only the KV tiles that a row tile sees are loaded, and only the kept query tiles that
- * see a KV tile are visited. */
+ * (lf_workspace_size; the forward needs none) and errors are theirs, and one operand more:
+ *   o_low  bf16 [T][hq][d], or NULL: what the rounding of o took away (o + o_low is O to
+ *          16 bits), written by the forward and read by the backward when it computes D
+ *          itself (D = NULL; with D given o_low must be NULL).  dS = P (dP - D) cancels for
+ *          rows whose weight lies on few keys, as caps, biases and masks make them, and there
+ *          D of the rounded o is the gradient's largest error: dQ of such rows came out up
+ *          to a tenth off.  With o_low it is dS's own rounding to bf16 that is left.
+ * The selection between the two is lf_block_select's (with D = NULL where o_low is used).
+ * prefix_len and row_start need causal = 1 (LF_ERR_UNSUPPORTED otherwise).  Device arrays
+ * of the modifier need only their type's alignment; their contents are checked on the
+ * device by the forward (a negative prefix by both): one that breaks its rule is reported
+ * by the next call (LF_ERR_INVALID_ARG), with the results undefined.  Only the KV tiles
+ * that a row tile sees are loaded, and only the kept query tiles that see a KV tile are
+ * visited. */
 lf_status lf_attn_fwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                          const void* k, const void* v, void* o, float* lse, void* ws,
-                          size_t ws_bytes, lf_stream_t stream);
+                          const void* k, const void* v, void* o, void* o_low, float* lse,
+                          lf_stream_t stream);
 lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, const void* q,
-                          const void* k, const void* v, const void* o, const float* lse,
-                          const void* dout, const float* D, const float* block_weight,
-                          const int32_t* kept_idx, const int32_t* kept_cnt, void* dq, void* dk,
-                          void* dv, void* ws, size_t ws_bytes, lf_stream_t stream);
+                          const void* k, const void* v, const void* o, const void* o_low,
+                          const float* lse, const void* dout, const float* D,
+                          const float* block_weight, const int32_t* kept_idx,
+                          const int32_t* kept_cnt, void* dq, void* dk, void* dv, void* ws,
+                          size_t ws_bytes, lf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Norms of the query and key heads with the position rotation (no counterpart in

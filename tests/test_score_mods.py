@@ -6,11 +6,17 @@ step of bf16, relative).
  * A score is a sum of d products in fp32: off by at most d u sum|q_i k_i| scale, plus 8 u of
    itself and of the bias, plus, when capped, 1e-6 of the cap's derivative times score
    (ez in all).  So LSE is off by ez + 16 u |LSE| + 1e-6, and P by 2 ez + 1e-6 of itself (ep).
- * O sums bf16 P (b of each term) and is rounded to bf16: (b + ep) sum P|V| + b |O|.
- * D comes from the bf16 O: off by |dO| . |O's error|.  dP is a sum of d products.
-   dS = w P (dP - D) (1 - tanh^2) is rounded to bf16: b + ep of itself, plus w P times the
-   errors of dP and D.  dQ = scale dS K, dK = scale dS^T Q and dV = (w P)^T dO pass these
-   through absolute values, add n u for their fp32 sums, and are rounded to bf16.
+ * O is the average of V with weights P^ = P (1 + e), each e the rounding of P to bf16 (b)
+   and ep, over their own sum: O - O_exact = sum (P^ - P) (V - O) is at most 2 (b + ep)
+   sum P|V - O| <= 2 (b + ep) sqrt(sum P (V - O)^2), and rounding to bf16 adds b |O|.
+ * D is <dO, O> with O's residual, so the same average of dP: off by 2 (b + ep) sum P|dP - D|
+   and b^2 of |dO|.|O|; where the selection gives D, from the rounded O, by b |dO|.|O| too.
+   dP is a sum of d products.  dS = w P (dP - D) (1 - tanh^2) is rounded to bf16: b + ep of
+   itself, plus w P times the errors of dP and D.  dQ = scale dS K, dK = scale dS^T Q and
+   dV = (w P)^T dO pass these through absolute values, add n u for their fp32 sums, and are
+   rounded to bf16.
+ * The plain forward divides by the exact sum of P instead: its O is off by (b + ep) sum P|V|
+   + b |O|, and its D by |dO| times that.
 """
 import ctypes
 import math
@@ -88,9 +94,10 @@ class Case:
         return torch.from_numpy(own)
 
 
-def reference(c, m, w=None):
+def reference(c, m, w=None, given_D=False, plain=False):
     """O, LSE, dQ, dK, dV of the formulas in 64 bits and how far the kernels' may be off.
-    w [nseq][hq][nb]: block weights (None: forward only)."""
+    w [nseq][hq][nb]: block weights (None: forward only); given_D: D is the selection's;
+    plain: the tolerances of the plain attention."""
     q, k, v, do = (m[x].double() for x in ("q", "k", "v", "dout"))
     out = {x: torch.zeros_like(m[y].double()) for x, y in (("o", "q"), ("dq", "q"), ("dk", "k"), ("dv", "v"))}
     out["lse"] = torch.zeros(c.hq, m["T"], dtype=torch.float64)
@@ -124,7 +131,10 @@ def reference(c, m, w=None):
             ep = 2 * ez + 1e-6
             o = p @ vh
             out["o"][r, h], out["lse"][h, r] = o, lse[:, 0]
-            eo = (B + ep) * (p @ vh.abs()) + B * o.abs()
+            if plain:
+                eo = (B + ep) * (p @ vh.abs()) + B * o.abs()
+            else:
+                eo = 2 * (B + ep) * (p @ vh.square() - o.square()).clamp(min=0).sqrt() + (B + 8 * U) * o.abs()
             tol["o"][r, h] = eo
             tol["lse"][h, r] = (ez + 16 * U * lse.abs() + 1e-6)[:, 0]
             if w is None:
@@ -133,8 +143,12 @@ def reference(c, m, w=None):
             dor = do[r, h]
             dp, D = dor @ vh.T, (dor * o).sum(1, keepdim=True)
             ds = wr * p * (dp - D) * damp
-            eD = (dor.abs() * eo).sum(1, keepdim=True)
             edp = c.d * U * (dor.abs() @ vh.abs().T)
+            if plain:
+                eD = (dor.abs() * eo).sum(1, keepdim=True)
+            else:
+                eD = 2 * (B + ep) * (p * (dp - D).abs()).sum(1, keepdim=True) + edp.amax(1, keepdim=True)
+                eD += ((B if given_D else B * B) + c.d * U) * (dor.abs() * o.abs()).sum(1, keepdim=True)
             eds = (B + ep + 4 * U) * ds.abs() + wr * p * damp * (eD + edp)
             if c.softcap:
                 eds = eds + wr * p * (dp - D).abs() * 2 * (ez / c.softcap + 1e-6)
@@ -155,24 +169,26 @@ def dev(m):
     return {n: t.cuda() if torch.is_tensor(t) else t for n, t in m.items()}
 
 
-def run(c, g, give_D=True, seed=3, extra=0):
+def run(c, g, give_D=False, seed=3, extra=0):
     desc, mod = c.desc(g, extra), c.mod(g)
     b = lf.Buffers(desc)
+    o_low = None if give_D else torch.empty_like(b.o)
     for t in (b.o, b.dq, b.dk, b.dv, b.lse):
         t.fill_(float("nan"))
-    lf.lf_attn_fwd_mod(desc, mod, g["q"], g["k"], g["v"], b.o, b.lse)
+    lf.lf_attn_fwd_mod(desc, mod, g["q"], g["k"], g["v"], b.o, b.lse, o_low)
     lf.lf_block_select(desc, g["dout"], b.o, c.delta, seed, 0, 0, b.norm, b.D if give_D else None, b.tau, b.w,
                        b.keep, b.kept_idx, b.kept_cnt)
     b.ws.fill_(255)
     lf.lf_attn_bwd_mod(desc, mod, g["q"], g["k"], g["v"], b.o, b.lse, g["dout"], b.D if give_D else None, b.w,
-                       b.kept_idx, b.kept_cnt, b.dq, b.dk, b.dv, b.ws)
+                       b.kept_idx, b.kept_cnt, b.dq, b.dk, b.dv, b.ws, o_low)
     lf.lf_sync_status()
     torch.cuda.synchronize()
+    b.o_low = o_low
     return b
 
 
-def check(c, m, b, parts=("o", "lse", "dq", "dk", "dv")):
-    ref, tol = reference(c, m, b.w.cpu() if "dq" in parts else None)
+def check(c, m, b, parts=("o", "lse", "dq", "dk", "dv"), given_D=False):
+    ref, tol = reference(c, m, b.w.cpu() if "dq" in parts else None, given_D)
     live = m["T"] - c.tail
     for x in parts:
         got, want, t = getattr(b, x).double().cpu(), ref[x], tol[x]
@@ -263,9 +279,38 @@ def test_training_step_matches_the_formula(c):
 
 @gpu
 @pytest.mark.parametrize("c", [CASES[0], CASES[19], CASES[22], CASES[25]], ids=lambda c: c.name)
-def test_row_products_computed_by_the_backward(c):
+def test_row_products_given_by_the_selection(c):
     m = c.make(2)
-    check(c, m, run(c, dev(m), give_D=False))
+    check(c, m, run(c, dev(m), give_D=True), given_D=True)
+
+
+@gpu
+@pytest.mark.parametrize("c", [CASES[0], CASES[5], CASES[13], CASES[24]], ids=lambda c: c.name)
+def test_residual_of_the_rounding(c):
+    """o + o_low is the unrounded O, o a nearest bf16 of it: o_low is at most half a step of o
+    (a power of two, so its own rounding to bf16 cannot pass it; on the tie o + o_low may
+    round to the other neighbour, which is why the sum is not compared with o)."""
+    m = c.make(9)
+    b = run(c, dev(m))
+    live = m["T"] - c.tail
+    o, low = b.o[:live].double(), b.o_low[:live].double()
+    half_step = torch.exp2(torch.floor(torch.log2(o.abs())) - 8)
+    assert (low.abs() <= half_step).all()
+    assert (low != 0).double().mean() > 0.9
+
+
+@gpu
+def test_a_row_on_one_key_gets_no_gradient():
+    """Softmax over one visible key is 1 whatever its score: dQ = 0, O = v, and dS = 0 but
+    for the errors of fp32 (D and dP are two sums of the same products)."""
+    c = Case("one", (40,), start=(np.arange(40),), softcap=20.0, alibi=True, spread=4.0)
+    m = c.make()
+    b = run(c, dev(m))
+    assert torch.equal(b.o.cpu(), m["v"].repeat_interleave(2, 1))
+    exact = (m["dout"].double().abs() * m["v"].double().abs().repeat_interleave(2, 1)).sum(2)   # [T, hq]
+    k = m["k"].double().abs().repeat_interleave(2, 1).amax(2)
+    w = torch.cat([b.w[0].cpu().double().T[[0]]] * 40)
+    assert (b.dq.double().cpu().abs().amax(2) <= 2 * c.d * U * w * exact * k * c.scale).all()
 
 
 @gpu
@@ -285,16 +330,15 @@ def test_a_mask_that_hides_nothing_is_the_plain_attention():
     p = lf.Buffers(desc)
     lf.lazyflash_step(desc, g["q"], g["k"], g["v"], g["dout"], 0.0, 3, 0, p)
     # the same scores, but the tiles in another order: the row's reference m differs, and with
-    # it where bf16 rounds each P (b of each term on either side: twice O's tolerance); in the
-    # row's sum of n <= 300 positive terms, kept in fp32, each addition, each exp2 (4 u) and
+    # it where bf16 rounds each P, so each side has its own tolerance; in the row's sum of n <= 300 positive terms, kept in fp32, each addition, each exp2 (4 u) and
     # each exponent (60 u of 1, |z - m| < 60) is off by as much on either side
-    tol = reference(c, m)[1]
-    assert ((b.o.double() - p.o.double()).abs().cpu() <= 2 * tol["o"]).all()
+    ours, plain = reference(c, m, b.w.cpu())[1], reference(c, m, b.w.cpu(), plain=True)[1]
+    assert ((b.o.double() - p.o.double()).abs().cpu() <= ours["o"] + plain["o"]).all()
     assert ((b.lse - p.lse).abs() <= 2 * (300 + 64) * U + 8 * U * p.lse.abs()).all()
     for x in ("dq", "dk", "dv"):   # dQ is summed by atomics, in any order
         # dS and P of the backward come from LSE and D; D from O (see the tolerances above)
         a, z = getattr(b, x).double().cpu(), getattr(p, x).double().cpu()
-        assert ((a - z).abs() <= 2 * reference(c, m, b.w.cpu())[1][x]).all()
+        assert ((a - z).abs() <= ours[x] + plain[x]).all()
 
 
 @gpu
@@ -546,19 +590,41 @@ def raw_desc(**kw):
 ])
 def test_bad_modifiers_rejected(L, mod, causal, code):
     d, m = raw_desc(causal=causal), lf.lf_score_mod(**mod)
-    assert L.lf_attn_fwd_mod(ctypes.byref(d), ctypes.byref(m), P, P, P, P, P, None, 0, None) == code
-    assert L.lf_attn_bwd_mod(ctypes.byref(d), ctypes.byref(m), *[P] * 14, 1 << 30, None) == code
+    assert L.lf_attn_fwd_mod(ctypes.byref(d), ctypes.byref(m), *fwd_args(), None) == code
+    assert L.lf_attn_bwd_mod(ctypes.byref(d), ctypes.byref(m), *bwd_args(), 1 << 30, None) == code
+
+
+def fwd_args(**kw):
+    return list(dict(dict(q=P, k=P, v=P, o=P, o_low=P, lse=P), **kw).values())
+
+
+def bwd_args(**kw):
+    return list(dict(dict(q=P, k=P, v=P, o=P, o_low=P, lse=P, dout=P, D=None, w=P, idx=P, cnt=P, dq=P, dk=P, dv=P, ws=P),
+                     **kw).values())
 
 
 def test_missing_modifier_operands_and_workspace_rejected(L):
     d, m = raw_desc(), lf.lf_score_mod(softcap=5.0, row_start=P)
-    assert L.lf_attn_fwd_mod(ctypes.byref(d), None, P, P, P, P, P, None, 0, None) == lf.LF_ERR_INVALID_ARG
-    assert L.lf_attn_fwd_mod(ctypes.byref(d), ctypes.byref(m), None, P, P, P, P, None, 0, None) == lf.LF_ERR_INVALID_ARG
-    assert L.lf_attn_fwd_mod(ctypes.byref(raw_desc(d=96)), ctypes.byref(m), P, P, P, P, P, None, 0, None) == lf.LF_ERR_UNSUPPORTED
+
+    def fwd(desc=d, mod=ctypes.byref(m), **kw):
+        return L.lf_attn_fwd_mod(ctypes.byref(desc), mod, *fwd_args(**kw), None)
+
+    def bwd(nbytes=1 << 30, desc=d, **kw):
+        return L.lf_attn_bwd_mod(ctypes.byref(desc), ctypes.byref(m), *bwd_args(**kw), nbytes, None)
+
+    assert fwd(mod=None) == lf.LF_ERR_INVALID_ARG
+    for x in ("q", "k", "v", "o", "lse"):
+        assert fwd(**{x: None}) == lf.LF_ERR_INVALID_ARG and fwd(**{x: P + 8}) == lf.LF_ERR_INVALID_ARG
+    assert fwd(o_low=P + 8) == lf.LF_ERR_INVALID_ARG
+    assert fwd(raw_desc(d=96)) == lf.LF_ERR_UNSUPPORTED
+    for x in ("q", "k", "v", "o", "lse", "dout", "w", "idx", "cnt", "dq", "dk", "dv"):
+        assert bwd(**{x: None}) == lf.LF_ERR_INVALID_ARG, x
+    assert bwd(D=P) == lf.LF_ERR_INVALID_ARG                 # D and the residual it would be computed with
+    assert bwd(o_low=P + 8) == lf.LF_ERR_INVALID_ARG
     n = ctypes.c_size_t(0)
     assert L.lf_workspace_size(ctypes.byref(d), lf.LF_WS_BWD, ctypes.byref(n)) == 0
-    assert L.lf_attn_bwd_mod(ctypes.byref(d), ctypes.byref(m), *[P] * 14, n.value - 1, None) == lf.LF_ERR_WORKSPACE
-    assert L.lf_attn_bwd_mod(ctypes.byref(raw_desc(total_tokens=0, max_seqlen=0)), ctypes.byref(m), *[P] * 14, 0, None) == 0
+    assert bwd(n.value - 1) == lf.LF_ERR_WORKSPACE and bwd(ws=None) == lf.LF_ERR_WORKSPACE
+    assert bwd(0, raw_desc(total_tokens=0, max_seqlen=0)) == 0
 
 
 def test_shared_prompt_tables_on_the_host():
