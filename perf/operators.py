@@ -375,12 +375,13 @@ def _attn_own(s):
         s["bufs"] = lf.Buffers(s["desc"]) if case["op"] == "attn_train" else None
         s["o"] = torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda")
         s["lse"] = torch.empty(hq, T, dtype=torch.float32, device="cuda")
-    lf.lf_attn_fwd_mod(s["desc"], s["mod"], s["q"], s["k"], s["v"], s["o"], s["lse"])
+        s["o_low"] = torch.empty_like(s["o"]) if case["op"] == "attn_train" else None
+    lf.lf_attn_fwd_mod(s["desc"], s["mod"], s["q"], s["k"], s["v"], s["o"], s["lse"], s["o_low"])
     if case["op"] == "attn_fwd":
         return s["o"], s["lse"]
     b = s["bufs"]
     lf.lf_attn_bwd_mod(s["desc"], s["mod"], s["q"], s["k"], s["v"], s["o"], s["lse"], s["dout"], None,
-                       s["weight"], s["kept_idx"], s["kept_cnt"], b.dq, b.dk, b.dv, b.ws)
+                       s["weight"], s["kept_idx"], s["kept_cnt"], b.dq, b.dk, b.dv, b.ws, s["o_low"])
     return s["o"], s["lse"], b.dq, b.dk, b.dv
 
 
