@@ -18,6 +18,7 @@ import itertools
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (Buffers, lf_attn_bwd, lf_attn_bwd_mod, lf_attn_fwd, lf_attn_fwd_mod, lf_block_select,
                lf_qk_norm_rope, lf_qk_norm_rope_bwd, lf_qk_workspace_size, make_desc, make_qk_desc,
@@ -119,6 +120,7 @@ class QkNormRope(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gq, gk):
         q, k, q_weight, k_weight = ctx.saved_tensors[:4]
         desc = ctx.desc

@@ -594,6 +594,11 @@ static lf_status attn_fwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod
     if (desc->total_tokens == 0 || desc->max_seqlen == 0) return LF_OK;
     if ((st = prepare_device()) != LF_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // an empty modifier runs the plain forward, which has no residual: 0, and its backward
+    // takes D from o alone
+    if (o_low && mod_variant(mod) == 0 &&
+        cudaMemsetAsync(o_low, 0, (size_t)desc->total_tokens * desc->hq * desc->d * 2, s) != cudaSuccess)
+        return LF_ERR_CUDA;
     return mirror_after(launch_fwd_any(desc, mod, q, k, v, o, o_low, lse, s), s);
 }
 

@@ -92,7 +92,8 @@ enum { LF_WS_FWD = 0, LF_WS_SELECT = 1, LF_WS_BWD = 2 };
 /* Flags of lf_block_select. */
 #define LF_SELECT_NORMS_GIVEN 0x1u  /* block_norm is an input; the norm pass only computes D */
 
-/* Bytes of workspace the call `which` (LF_WS_*) needs for `desc`.
+/* Bytes of workspace the call `which` (LF_WS_*) needs for `desc`; LF_WS_BWD covers
+ * lf_attn_bwd and lf_attn_bwd_mod.
  * Returns LF_ERR_INVALID_ARG / LF_ERR_UNSUPPORTED for a bad descriptor. */
 lf_status lf_workspace_size(const lf_attn_desc* desc, int which, size_t* bytes);
 
@@ -239,8 +240,8 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
  * ------------------------------------------------------------------------- */
 typedef struct {
     float softcap;               /* 0: none; else in [1e-3, 1e6] */
-    const float* alibi_slopes;   /* DEVICE [hq], or NULL: no bias.  No gradient is computed for it.  The
-                                    distance counts rows of the packed segment */
+    const float* alibi_slopes;   /* DEVICE [hq], finite, of either sign, or NULL: no bias.  No gradient is
+                                    computed for it.  The distance counts rows of the packed segment */
     const int32_t* prefix_len;   /* DEVICE [nseq], >= 0 (beyond the segment: the whole segment), or NULL */
     int32_t prefix_causal;       /* 0 or 1 (1 only with prefix_len) */
     const int32_t* row_start;    /* DEVICE [total_tokens], or NULL.  Within a segment 0 <= row_start[t] <= t,
@@ -255,7 +256,8 @@ typedef struct {
  *          itself (D = NULL; with D given o_low must be NULL).  dS = P (dP - D) cancels for
  *          rows whose weight lies on few keys, as caps, biases and masks make them, and there
  *          D of the rounded o is the gradient's largest error: dQ of such rows came out up
- *          to a tenth off.  With o_low it is dS's own rounding to bf16 that is left.
+ *          to a tenth off.  With o_low it is dS's own rounding to bf16 that is left.  (An
+ *          empty modifier is the plain attention: o_low is then all 0.)
  * The selection between the two is lf_block_select's (with D = NULL where o_low is used).
  * prefix_len and row_start need causal = 1 (LF_ERR_UNSUPPORTED otherwise).  Device arrays
  * of the modifier need only their type's alignment; their contents are checked on the
@@ -281,7 +283,9 @@ lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, con
  *   n = w * x / sqrt(mean(x^2) + eps) over the d values of one head of one token
  *   (n = x without LF_QK_NORM), then for every rotated pair (a, b) with angle
  *   index i: y_a = n_a cos_i - n_b sin_i, y_b = n_b cos_i + n_a sin_i; columns at
- *   or past `rot` are not rotated.  Computed in fp32 and rounded once to bf16.
+ *   or past `rot` are not rotated.  Computed in fp32 and rounded once to bf16; the
+ *   squares' sum too, so values have to stay below about 1e18, and a row of zeros
+ *   needs eps > 0.
  * ------------------------------------------------------------------------- */
 
 /* Which columns of a head form pair i, i in [0, rot/2). */

@@ -44,7 +44,7 @@ def window(n, w):
 
 class Case:
     def __init__(self, name, lens, hq=4, hkv=2, d=128, block=128, softcap=0.0, alibi=False, prefix=None,
-                 prefix_causal=False, start=None, causal=True, spread=1.5, tail=0, delta=0.2):
+                 prefix_causal=False, start=None, causal=True, spread=1.5, tail=0, delta=0.2, rising=False):
         self.__dict__.update(locals())
         del self.__dict__["self"]
 
@@ -67,6 +67,8 @@ class Case:
         m["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(self.lens)]), dtype=torch.int32)
         m["nb"] = nb
         m["slopes"] = torch.tensor([0.7 * 2.0 ** (-4 * h / self.hq) for h in range(self.hq)]) if self.alibi else None
+        if self.rising:   # every other head's bias grows with the distance
+            m["slopes"][1::2] *= -0.1
         m["prefix"] = None if self.prefix is None else torch.tensor(self.prefix, dtype=torch.int32)
         m["start"] = None
         if self.start is not None:
@@ -237,6 +239,10 @@ CASES = [
     Case("odd_group", (333, 200), hq=6, hkv=2, softcap=9.0, alibi=True),
     Case("many_segments", (0, 1, 127, 128, 129, 256, 300, 5) * 5, hq=2, hkv=1, d=64, block=64, softcap=5.0,
          start=[window(n, 70) for n in (0, 1, 127, 128, 129, 256, 300, 5) * 5]),
+    Case("rising_bias", (400, 129), alibi=True, rising=True),
+    Case("rising_bias_capped", (300, 260), d=64, alibi=True, rising=True, softcap=9.0, start=(window(300, 200), documents((130, 130)))),
+    Case("high_cap_bias", (300, 200), alibi=True, softcap=100.0, spread=3.0, prefix=(20, 150)),
+    Case("high_cap", (520,), hq=2, hkv=2, softcap=60.0, spread=6.0, start=(window(520, 256),)),
     Case("padded", (200, 100), alibi=True, start=(window(200, 150), documents((50, 50))), tail=90),
 ]
 # every compiled variant: which modifiers x head dim x block rows
@@ -248,6 +254,7 @@ for bits in range(1, 8):
                               **(dict(prefix=(70, 0), prefix_causal=True,
                                       start=(documents((130, 100, 60)), window(150, 33))) if bits & 4 else {})))
 each = pytest.mark.parametrize("c", CASES, ids=lambda c: c.name)
+NAMED = {c.name: c for c in CASES}
 
 
 @gpu
@@ -278,14 +285,14 @@ def test_training_step_matches_the_formula(c):
 
 
 @gpu
-@pytest.mark.parametrize("c", [CASES[0], CASES[19], CASES[22], CASES[25]], ids=lambda c: c.name)
+@pytest.mark.parametrize("c", [NAMED["cap"], NAMED["window_and_kept_prefix"], NAMED["prompt_64"], NAMED["everything_64"]], ids=lambda c: c.name)
 def test_row_products_given_by_the_selection(c):
     m = c.make(2)
     check(c, m, run(c, dev(m), give_D=True), given_D=True)
 
 
 @gpu
-@pytest.mark.parametrize("c", [CASES[0], CASES[5], CASES[13], CASES[24]], ids=lambda c: c.name)
+@pytest.mark.parametrize("c", [NAMED["cap"], NAMED["bias"], NAMED["documents"], NAMED["everything"]], ids=lambda c: c.name)
 def test_residual_of_the_rounding(c):
     """o + o_low is the unrounded O, o a nearest bf16 of it: o_low is at most half a step of o
     (a power of two, so its own rounding to bf16 cannot pass it; on the tie o + o_low may
@@ -314,7 +321,7 @@ def test_a_row_on_one_key_gets_no_gradient():
 
 
 @gpu
-@pytest.mark.parametrize("c", [CASES[13], CASES[20], CASES[28]], ids=lambda c: c.name)
+@pytest.mark.parametrize("c", [NAMED["documents"], NAMED["prompt"], NAMED["many_segments"]], ids=lambda c: c.name)
 def test_max_seqlen_above_the_longest_segment(c):
     m = c.make(3)
     check(c, m, run(c, dev(m), extra=333))
@@ -342,7 +349,7 @@ def test_a_mask_that_hides_nothing_is_the_plain_attention():
 
 
 @gpu
-@pytest.mark.parametrize("c", [CASES[13], CASES[16], CASES[19], CASES[20], CASES[24]], ids=lambda c: c.name)
+@pytest.mark.parametrize("c", [NAMED["documents"], NAMED["window"], NAMED["window_and_kept_prefix"], NAMED["prompt"], NAMED["everything"]], ids=lambda c: c.name)
 def test_hidden_keys_do_not_matter(c):
     """Bit for bit: keys and values that a row does not see may be anything finite, and the
     output gradient of rows that do not see a key does not reach it."""
@@ -380,7 +387,7 @@ def test_hidden_keys_do_not_matter(c):
 
 
 @gpu
-@pytest.mark.parametrize("c", [CASES[0], CASES[6], CASES[11], CASES[24]], ids=lambda c: c.name)
+@pytest.mark.parametrize("c", [NAMED["cap"], NAMED["bias_not_causal"], NAMED["prefix_bias"], NAMED["everything"]], ids=lambda c: c.name)
 def test_gradient_matches_differences(c):
     """The weighted sum sum(w dO O) along a direction that agrees with the kernel's gradient
     in every sign, by central differences of the formula in 64 bits (their own error is the
@@ -454,8 +461,53 @@ def test_layer_with_a_shared_prompt_equals_separate_copies():
 
 
 @gpu
+def test_an_empty_modifier_is_the_plain_attention():
+    c = Case("empty", (200, 57))
+    m = c.make()
+    g = dev(m)
+    b, desc = run(c, g), c.desc(g)
+    p = lf.Buffers(desc)
+    lf.lazyflash_step(desc, g["q"], g["k"], g["v"], g["dout"], c.delta, 3, 0, p)
+    assert torch.equal(b.o, p.o) and torch.equal(b.lse, p.lse) and (b.o_low == 0).all()
+    assert torch.equal(b.dk, p.dk) and torch.equal(b.dv, p.dv)
+    assert (b.dq.float() - p.dq.float()).norm() <= B * p.dq.float().norm()
+
+
+@gpu
+def test_slices_of_longer_arrays_and_two_streams_at_once():
+    """The modifier's arrays need only four bytes of alignment, and two calls with buffers of
+    their own may run at the same time."""
+    c = NAMED["everything"]
+    m = c.make()
+    g = dev(m)
+    want = run(c, g)
+    for x in ("slopes", "start", "prefix"):
+        g[x] = torch.cat([g[x][:1], g[x]])[1:]
+        assert g[x].data_ptr() % 16
+    desc, mod = c.desc(g), c.mod(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            b = lf.Buffers(desc)
+            low = torch.empty_like(b.o)
+            for _ in range(3):
+                lf.lf_attn_fwd_mod(desc, mod, g["q"], g["k"], g["v"], b.o, b.lse, low)
+                lf.lf_attn_bwd_mod(desc, mod, g["q"], g["k"], g["v"], b.o, b.lse, g["dout"], None, want.w,
+                                   want.kept_idx, want.kept_cnt, b.dq, b.dk, b.dv, b.ws, low)
+            outs.append(b)
+    torch.cuda.synchronize()
+    lf.lf_sync_status()
+    for b in outs:
+        assert torch.equal(b.o, want.o) and torch.equal(b.lse, want.lse)
+        assert torch.equal(b.dk, want.dk) and torch.equal(b.dv, want.dv)
+        assert (b.dq.float() - want.dq.float()).norm() <= B * want.dq.float().norm()
+
+
+@gpu
 def test_autograd_passes_the_modifier_on():
-    c = CASES[24]
+    c = NAMED["everything"]
     m = c.make(6)
     g = dev(m)
     q, k, v = (g[x].clone().requires_grad_(True) for x in ("q", "k", "v"))
@@ -470,7 +522,7 @@ def test_autograd_passes_the_modifier_on():
 
 @gpu
 def test_side_stream_and_captured_graph():
-    c = CASES[25]
+    c = NAMED["everything_64"]
     m = c.make(7)
     g = dev(m)
     b = run(c, g)
@@ -637,7 +689,7 @@ def test_shared_prompt_tables_on_the_host():
 
 @gpu
 def test_binding_refuses_what_does_not_fit():
-    c = CASES[24]
+    c = NAMED["everything"]
     g = dev(c.make())
     desc, mod = c.desc(g), c.mod(g)
     o, lse = torch.empty_like(g["q"]), torch.empty(c.hq, g["T"], device="cuda")
