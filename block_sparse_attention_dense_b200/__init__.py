@@ -285,6 +285,8 @@ def lf_attn_bwd_static_ws(desc, q, k, v, o, lse, dout, D, block_weight, kept_idx
 def _on_device(device, call, stream):
     """call(stream pointer) with `device` current, on torch's current stream of that
     device unless a stream is given."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)   # as an integer: no Stream object
     if torch.cuda.current_device() == device.index:
         return call(_stream(stream))
     with torch.cuda.device(device):
@@ -438,19 +440,20 @@ def make_qk_desc(q, k, q_weight=None, k_weight=None, cos_sin=None, cu_seqlens=No
         _vector(q_weight, "q_weight", dev, floats, d), _vector(k_weight, "k_weight", dev, floats, d),
         int(bool(ws) and ws[0].dtype == torch.bfloat16))
     desc._keepalive = (q_weight, k_weight, cos_sin, cu_seqlens, positions)
-    desc._device = dev
+    desc._device, desc._index, desc._tokens_and_dim = dev, dev.index, (T, d)
+    desc._heads = (hq, k.shape[1])
     return desc
 
 
 def _rows(t, desc, heads, name):
     """Address and token stride of a [T, heads, d] bf16 operand whose heads are contiguous."""
-    T, d = desc.total_tokens, desc.d
-    if t.dtype != torch.bfloat16 or t.device != desc._device or tuple(t.shape) != (T, heads, d):
+    T, d = desc._tokens_and_dim
+    if t.dtype is not torch.bfloat16 or t.get_device() != desc._index or t.shape != (T, heads, d):
         raise ValueError("%s must be a bf16 [%d, %d, %d] tensor on %s" % (name, T, heads, d, desc._device))
-    s = t.stride()
-    if T and (s[2] != 1 or (heads > 1 and s[1] != d)):
+    token, head, one = t.stride()
+    if T and (one != 1 or (heads > 1 and head != d)):
         raise ValueError("%s must have contiguous heads" % name)
-    return t.data_ptr(), (s[0] if T > 1 else heads * d)
+    return t.data_ptr(), (token if T > 1 else heads * d)
 
 
 def lf_qk_workspace_size(desc: lf_qk_desc) -> int:
@@ -460,8 +463,9 @@ def lf_qk_workspace_size(desc: lf_qk_desc) -> int:
 
 
 def lf_qk_norm_rope(desc, q, k, q_out, k_out, stream=None):
-    args = (*_rows(q, desc, desc.hq, "q"), *_rows(k, desc, desc.hkv, "k"),
-            *_rows(q_out, desc, desc.hq, "q_out"), *_rows(k_out, desc, desc.hkv, "k_out"))
+    hq, hkv = desc._heads
+    args = (*_rows(q, desc, hq, "q"), *_rows(k, desc, hkv, "k"),
+            *_rows(q_out, desc, hq, "q_out"), *_rows(k_out, desc, hkv, "k_out"))
     _check(_on_device(desc._device, lambda s: _load().lf_qk_norm_rope(ctypes.byref(desc), *args, s),
                       stream), "lf_qk_norm_rope")
 
