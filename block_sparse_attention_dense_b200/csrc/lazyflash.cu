@@ -148,7 +148,7 @@ lf::ModParams mod_params(const lf_attn_desc* d, const lf_score_mod* m) {
         p.cap_damp = static_cast<float>(-1.0 / (c * c));
         for (int i = 0; i < lf::kCapTerms; ++i) p.cap_coef[i] = static_cast<float>(c * lf::kCapCoef[i]);
         const double a = (double)d->softmax_scale / m->softcap;
-        const bool fits = a >= 1e-5 && a <= 1e4;   // every C a^(2k+1) is a normal number
+        const bool fits = a >= 3e-4 && a <= 1e3;   // every C a^(2k+1) is a normal number
         for (int i = 0; i < lf::kCapFusedTerms; ++i)
             p.cap_fused[i] = fits ? static_cast<float>(c * lf::kCapFused[i] * std::pow(a, 2 * i + 1)) : 0.f;
         p.fused_max = fits ? static_cast<float>(lf::kCapFusedRange / a) : 0.f;

@@ -20,18 +20,20 @@ enum { kModCap = 1, kModBias = 2, kModMask = 4 };
 // tanh(x) = x p(x^2), p a relative minimax fit (iterated weighted least squares on Chebyshev
 // nodes, in double).  tanh.approx (2^-11) would cost the scores three digits, and exp and a
 // reciprocal two more operations of the unit that the softmax already fills.
-//  * kCapFused: |x| <= 1/2, degree three, off by 5.5e-7 of tanh.  The scale goes into the
+//  * kCapFused: |x| <= 0.7, degree four, off by 3.1e-7 of tanh.  The scale goes into the
 //    coefficients (C a^(2k+1) c_k, powers of s), which holds while those stay normal numbers
-//    (the host sets fused_max to 0 where they would not), and the last product into the
-//    exponent's FMA: four packed operations a pair instead of the uncapped one.
+//    (the host sets fused_max to 0 where they would not): six packed operations a pair
+//    instead of the uncapped one.  Degree three (to 0.5) made the forward 6 % faster where
+//    all scores lie within it, and three times slower where some do not (16,384 tokens,
+//    scores of deviation 2: cap 50 2.22 against 2.36 ms, cap 14 6.4 against 2.8 ms).
 //  * kCapCoef: |x| <= 3/4, degree five, off by 2.9e-8, and 1.6e-7 in fp32; beyond,
 //    1 - 2 / (1 + exp(2 |x|)), whose error is below 4e-7 of tanh there.
 // A warp (or, in the gradient, a chunk of 16 columns) whose scores all lie within the first
 // takes it, else the second for all of them.
-constexpr int kCapFusedTerms = 4;
-constexpr double kCapFused[kCapFusedTerms] = {0.999999455771, -0.333263179339, 0.131902965817,
-                                              -0.044402225555};
-constexpr double kCapFusedRange = 0.5;
+constexpr int kCapFusedTerms = 5;
+constexpr double kCapFused[kCapFusedTerms] = {0.999999697294, -0.333302129002, 0.132811125731,
+                                              -0.050836235324, 0.013773709951};
+constexpr double kCapFusedRange = 0.7;
 constexpr float kCapRange = 0.75f;
 constexpr int kCapTerms = 6;
 constexpr double kCapCoef[kCapTerms] = {0.999999971014, -0.333329588792, 0.133254060138,
