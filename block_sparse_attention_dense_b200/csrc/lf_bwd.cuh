@@ -43,7 +43,9 @@
 // capped and biased score, dS takes the cap's derivative 1 - tanh^2, and under a mask the
 // CTA visits only the kept query tiles between the first row that may see its keys and the
 // last one that does; within them, the rows that see a key are one run, so that a thread
-// (one key) compares the query's index with two bounds.
+// (one key) compares the query's index with two bounds, and not at all in halves that hide
+// nothing.  16,384 tokens, 32/8 heads of 128, causal, 30 % of the blocks kept, plain
+// 1.92 ms: cap 2.27, bias 1.97, a mask that hides nothing 2.16, a window of 1,024 keys 0.50.
 //
 // Tensor memory (512 columns): dV [0,128) dK [128,256); half 0: S^T [256,320)
 // (after the element-wise pass: P^T in its first 32 columns, dS^T in the next 32,

@@ -24,11 +24,16 @@
 // of a region by a later MMA relies on tcgen05.mma executing in issue order.
 //
 // kMod selects modified scores (lf_mod.cuh) at compile time: the tanh cap and the distance
-// bias in the softmax warps, before the row maximum; the masks also in the KV tiles that
-// are visited.  Under a mask the two query tiles of a CTA share one list of KV tiles (the
-// prefix's, then a run up to the diagonal), and a tile that has nothing in a step only
-// hands the step's stages back, so that a document's end between the two does not make the
-// later one walk the earlier one's keys.
+// bias in the softmax warps, the masks also in the KV tiles that are visited.  KV tiles are
+// then taken from the diagonal down, so that a row has its reference from its first tile.
+// Under a mask the two query tiles of a CTA share one list of KV tiles (the prefix's, and a
+// run up to the diagonal), and a tile that has nothing in a step only hands the step's
+// stages back, so that a document's end between the two does not make the later one walk
+// the earlier one's keys.  A row's softmax warp is bound by its own latency (the exp2 unit
+// and the FMA pipes are busy 45 and 36 % of the time under a cap), so the cap and the bias
+// are laid beside the exp2 (capped_row; `fused`).  16,384 tokens, 32/8 heads of 128, causal,
+// plain 1.72 ms: cap 2.36, bias 1.86, a mask that hides nothing 1.87, both cap and bias
+// 2.9-3.1, a window of 1,024 keys 0.45 ms.
 #pragma once
 
 #include <climits>

@@ -16,8 +16,8 @@
 // heads', so that the token's cosines and sines (in the forward with the norm weights
 // multiplied in) stay in registers for all of them; with few tokens a token's row groups
 // are spread over several warps instead (see qk_grid in lazyflash.cu).
-// 32,768 tokens, 32/8 heads of 128, on one B200: forward 134 us (80 % of the measured copy
-// bandwidth), gradient 211 us (75 %).  With one 16-byte chunk per lane and partners fetched
+// 32,768 tokens, 32/8 heads of 128, on one B200: forward 131 us (81 % of the measured copy
+// bandwidth), gradient 208 us (76 %).  With one 16-byte chunk per lane and partners fetched
 // by shuffles it was 162 and 348 us: 100 and 145 registers left 16 and 8 warps per SM.
 //
 // The weight gradients are summed in a fixed order: each lane over its rows, the warp and

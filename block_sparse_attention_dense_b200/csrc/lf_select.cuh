@@ -470,10 +470,10 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float4* __restric
 // passed no D), compute D = <dO_t, O_t> for the kept blocks' rows and write 0 for the
 // dropped blocks' rows (the backward reads them, with weight 0, when a 128-row tile
 // holds one kept and one dropped 64-row block).  kMod (modified scores): with o_low, O's
-// rounding residual from the forward, D is that of the unrounded O; with key_last (
-// per-row starts) the head-0 CTAs also find, for each of the block's keys, the last row of
-// the segment that sees it: one bisection per key, here rather than in the backward's CTAs,
-// each of which would repeat it for every head group.
+// rounding residual from the forward, D is that of the unrounded O; with key_last (masks
+// with per-row starts) the head-0 CTAs also find, for each of the block's keys, the last
+// row of the segment that sees it: one bisection per key, here rather than in the
+// backward's CTAs, each of which would repeat it for every head group.
 template <int D, bool kMod>
 __global__ void __launch_bounds__(kNormThreads) bwd_prologue_kernel(
     const int32_t* __restrict__ cu_seqlens, int T, int max_seqlen, int H, int block_q, int nbmax,

@@ -37,7 +37,8 @@
  *     launched (LF_ERR_INVALID_ARG, LF_ERR_UNSUPPORTED, LF_ERR_WORKSPACE).
  *     A failed launch returns LF_ERR_CUDA.  Kernels never hang: a kernel whose
  *     bounded wait expired (LF_ERR_TIMEOUT), or that found cu_seqlens
- *     inconsistent with total_tokens / max_seqlen (LF_ERR_INVALID_ARG), records
+ *     inconsistent with total_tokens / max_seqlen, a rotation position outside
+ *     its table or a mask that breaks its rules (LF_ERR_INVALID_ARG), records
  *     the failure in a device flag and returns.  The failure is reported
  *     (1) by the next call of any entry point made after the failing call's
  *     work finished: every call that launches work ends with a one-thread
