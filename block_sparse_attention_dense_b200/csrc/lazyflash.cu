@@ -467,14 +467,7 @@ __global__ void watchdog_selftest_kernel(long long limit) {
 // Enqueued at the end of every call that launches kernels: copies the failure flag,
 // once set, into the host-mapped page, so that the next call sees it without a
 // synchronization.
-__global__ void mirror_error_kernel() {
-    const int e = *reinterpret_cast<volatile int*>(&g_device_error);
-    int* m = g_error_mirror;
-    if (e != 0 && m) {
-        *reinterpret_cast<volatile int*>(m) = e;
-        __threadfence_system();
-    }
-}
+__global__ void mirror_error_kernel() { mirror_error(); }
 }  // namespace lf
 
 // Scratch of lf_attn_bwd_static_ws: one array per device, loaded with the
@@ -599,7 +592,9 @@ static lf_status attn_fwd_impl(const lf_attn_desc* desc, const lf_score_mod* mod
     if (o_low && mod_variant(mod) == 0 &&
         cudaMemsetAsync(o_low, 0, (size_t)desc->total_tokens * desc->hq * desc->d * 2, s) != cudaSuccess)
         return LF_ERR_CUDA;
-    return mirror_after(launch_fwd_any(desc, mod, q, k, v, o, o_low, lse, s), s);
+    st = launch_fwd_any(desc, mod, q, k, v, o, o_low, lse, s);
+    // the variants with modified scores write the host page themselves: one launch fewer
+    return mod_variant(mod) == 0 ? mirror_after(st, s) : st;
 }
 
 lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, const void* v,

@@ -33,6 +33,16 @@ constexpr long long kWaitLimitCycles = 1ll << 31;   // ~1.1 s at 1.9 GHz
 __device__ __forceinline__ void report_error(int site, int kind) {
     atomicCAS(&g_device_error, 0, (site << 8) | kind);
 }
+// Copies a recorded failure to the host-mapped page: by the kernels that no mirroring
+// kernel follows, on their way out after a failure.
+__device__ __forceinline__ void mirror_error() {
+    const int e = *reinterpret_cast<volatile int*>(&g_device_error);
+    int* m = g_error_mirror;
+    if (e != 0 && m) {
+        *reinterpret_cast<volatile int*>(m) = e;
+        __threadfence_system();
+    }
+}
 __device__ __forceinline__ void report_timeout(int site) { report_error(site, kErrTimeout); }
 
 // Reads segment s of the segment table and checks it against the sizes the

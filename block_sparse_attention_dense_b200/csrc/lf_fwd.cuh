@@ -269,7 +269,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int s = segment_of_unit(prm.cu_seqlens, prm.nseq, pg, 8);
     if (s < 0) return;
     int seg0, len;
-    if (!load_segment(prm.cu_seqlens, s, prm.T, prm.max_seqlen, seg0, len, 20)) return;
+    if (!load_segment(prm.cu_seqlens, s, prm.T, prm.max_seqlen, seg0, len, 20)) {
+        if (kMod != 0 && threadIdx.x == 0) mirror_error();
+        return;
+    }
     const int ntiles = (len + 127) >> 7;
     const int npairs = (ntiles + 1) >> 1;
     const int m = npairs - 1 - (pg - first_unit_of_segment(seg0, s, 8));   // longest rows first
@@ -284,7 +287,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if constexpr (kMask) {
         bool bad = false;
         P = prefix_of(prm.mod, s, len, bad);
-        if (bad && threadIdx.x == 0) report_error(17, kErrBadMask);
+        if (bad && threadIdx.x == 0) {
+            report_error(17, kErrBadMask);
+            mirror_error();
+        }
         runs0 = tile_runs(prm.mod, 2 * m, seg0, len, P);
         runs1 = two ? tile_runs(prm.mod, 2 * m + 1, seg0, len, P) : TileRuns{0, 0, 0};
         runs1.lo = max(runs1.lo, runs0.lo);   // starts never decrease; all roles rely on it
@@ -461,7 +467,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 publish(INT_MAX);   // finished (or aborted): never hold the other issuer
                 mma_commit_warp(&bar_done[t]);
                 // every MMA issued by this warp has finished (waits even after an abort)
-                __all_sync(0xffffffffu, mbar_wait(&bar_done[t], 0, 29));
+                const bool drained = __all_sync(0xffffffffu, mbar_wait(&bar_done[t], 0, 29));
+                if (kMod != 0 && !drained) *abort_flag = 1;
             }
         }
     } else {
@@ -495,7 +502,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const int row = min(q_local, len - 1);
                 from = rs[row];
                 // starts lie in the row's own past and never decrease
-                if (from < 0 || from > row || (row + 1 < len && rs[row + 1] < from)) report_error(16, kErrBadMask);
+                if (from < 0 || from > row || (row + 1 < len && rs[row + 1] < from)) {
+                    report_error(16, kErrBadMask);
+                    mirror_error();
+                }
                 from = min(max(from, 0), row);
                 all_from = min(max(rs[min(qt * 128 + 127, len - 1)], 0), len - 1);
             }
@@ -769,6 +779,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (kMod != 0 && tid == 0 && *abort_flag) mirror_error();   // no mirroring kernel follows
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

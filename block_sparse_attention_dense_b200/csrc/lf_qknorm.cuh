@@ -52,17 +52,6 @@ struct QkParams {
     float* partial;                  // backward: [blocks][2][d], or null
 };
 
-// A failure that the next call has to see: the flag, and its host-mapped copy at once
-// (these kernels are not followed by the mirroring kernel).
-__device__ __forceinline__ void report_error_now(int site, int kind) {
-    report_error(site, kind);
-    int* m = g_error_mirror;
-    if (m) {
-        *reinterpret_cast<volatile int*>(m) = (site << 8) | kind;
-        __threadfence_system();
-    }
-}
-
 // Four bf16 of a row as two packed pairs.
 struct Four {
     float2 lo, hi;
@@ -320,7 +309,10 @@ __global__ void __launch_bounds__(kQkThreads, kBack ? kQkBlocksBwd : kQkBlocksFw
         const int g0 = static_cast<int>(unit - (long long)t * p.units_per_token) * p.per_unit;
         const int g1 = min(ng, g0 + p.per_unit);
         const bool live = pos >= 0, skip = !live && (bad || !p.zero_tail);
-        if (bad && lane == 0) report_error_now(60, kErrBadPosition);
+        if (bad && lane == 0) {
+            report_error(60, kErrBadPosition);
+            mirror_error();
+        }
         LaneAngles<kPairs> an;
         an.load(p.cos_sin + (size_t)max(pos, 0) * p.rot, l, p.rot, col.on && live, kBack);
         // the next unit's position is on its way while this unit's rows are

@@ -43,7 +43,8 @@
  *     (1) by the next call of any entry point made after the failing call's
  *     work finished: every call that launches work ends with a one-thread
  *     kernel that copies the flag into a page of host memory mapped into the
- *     device, so this check needs no synchronization; that call returns the
+ *     device (lf_attn_fwd_mod, lf_qk_norm_rope and its gradient write that page
+ *     themselves), so this check needs no synchronization; that call returns the
  *     code and launches nothing; every later call does the same until the
  *     failure is cleared; and (2) by lf_sync_status (alias
  *     lf_check_device_error), which synchronizes the stream, returns the code
