@@ -96,6 +96,8 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     distance; no gradient), ``prefix_len`` [nseq], ``prefix_causal`` and ``row_start`` [T]
     (prefix, document, window and shared-prompt masks) modify the scores of both directions:
     lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's."""
+    if alibi_slopes is not None and alibi_slopes.requires_grad:
+        raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
     mod = None
     if softcap or alibi_slopes is not None or prefix_len is not None or row_start is not None or prefix_causal:
         mod = make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)

@@ -610,6 +610,7 @@ lf_status lf_attn_fwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, con
     lf_status st = check_desc(desc);
     if (st == LF_OK) st = check_mod(desc, mod);
     if (st == LF_OK && !aligned16(o_low)) st = LF_ERR_INVALID_ARG;
+    if (st == LF_OK && desc->total_tokens == 0) return pending_device_error();   // empty tensors have no address
     return st != LF_OK ? st : attn_fwd_impl(desc, mod, q, k, v, o, o_low, lse, stream);
 }
 
@@ -730,6 +731,7 @@ lf_status lf_attn_bwd_mod(const lf_attn_desc* desc, const lf_score_mod* mod, con
     lf_status st = check_desc(desc);
     if (st == LF_OK) st = check_mod(desc, mod);
     if (st == LF_OK && (!aligned16(o_low) || (o_low && D))) st = LF_ERR_INVALID_ARG;
+    if (st == LF_OK && desc->total_tokens == 0) return pending_device_error();
     return st != LF_OK ? st
                        : attn_bwd_impl(desc, mod, q, k, v, o, o_low, lse, dout, D, block_weight, kept_idx, kept_cnt, dq,
                                        dk, dv, ws, ws_bytes, stream);

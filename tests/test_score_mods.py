@@ -676,7 +676,9 @@ def test_missing_modifier_operands_and_workspace_rejected(L):
     n = ctypes.c_size_t(0)
     assert L.lf_workspace_size(ctypes.byref(d), lf.LF_WS_BWD, ctypes.byref(n)) == 0
     assert bwd(n.value - 1) == lf.LF_ERR_WORKSPACE and bwd(ws=None) == lf.LF_ERR_WORKSPACE
-    assert bwd(0, raw_desc(total_tokens=0, max_seqlen=0)) == 0
+    none = raw_desc(total_tokens=0, max_seqlen=0)   # an empty batch, whose tensors have no address
+    assert fwd(none, **dict.fromkeys(("q", "k", "v", "o", "o_low", "lse"))) == 0
+    assert bwd(0, none, **dict.fromkeys(("q", "k", "v", "o", "o_low", "lse", "dout", "dq", "dk", "dv", "ws"))) == 0
 
 
 def test_shared_prompt_tables_on_the_host():
@@ -685,6 +687,12 @@ def test_shared_prompt_tables_on_the_host():
     assert start.tolist() == [0, 0, 0, 3, 3, 5, 0, 0] and pos.tolist() == [0, 1, 2, 3, 4, 3, 0, 1]
     with pytest.raises(ValueError):
         lf.shared_prompt_tables([3], [[1], [2]], device="cpu")
+
+
+def test_slopes_that_ask_for_a_gradient_are_refused():
+    x, slopes = torch.zeros(4, 2, 64), torch.zeros(2, requires_grad=True)
+    with pytest.raises(ValueError, match="slopes"):
+        lazyflash_attention(x, x, x, torch.tensor([0, 4]), 4, alibi_slopes=slopes)
 
 
 @gpu
