@@ -368,7 +368,7 @@ def lf_attn_bwd_mod(desc, mod, q, k, v, o, lse, dout, D, block_weight, kept_idx,
         ("o", o, desc.hq), ("o_low", o_low, desc.hq), ("lse", lse, rows), ("dout", dout, desc.hq), ("D", D, rows),
         ("block_weight", block_weight, (torch.float32, nb)), ("kept_idx", kept_idx, (torch.int32, nb)),
         ("kept_cnt", kept_cnt, (torch.int32, heads)), ("dq", dq, desc.hq), ("dk", dk, desc.hkv),
-        ("dv", dv, desc.hkv)])
+        ("dv", dv, desc.hkv), ("ws", ws, (torch.uint8, None))])
     L = _load()
     args = [None if t is None else t.data_ptr()
             for t in (q, k, v, o, o_low, lse, dout, D, block_weight, kept_idx, kept_cnt, dq, dk, dv, ws)]

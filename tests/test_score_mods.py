@@ -714,3 +714,8 @@ def test_binding_refuses_what_does_not_fit():
             lf.make_score_mod(**kw)
     with pytest.raises(ValueError):
         lf.lf_attn_fwd_mod(desc, mod, g["q"], g["k"], g["v"], o, lse.double())
+    b = lf.Buffers(desc)
+    args = [g["q"], g["k"], g["v"], o, lse, g["dout"], None, b.w, b.kept_idx, b.kept_cnt, b.dq, b.dk, b.dv, b.ws]
+    for i, bad in ((6, b.D.double()), (7, b.w[:, :1]), (8, b.kept_idx.long()), (10, b.dk), (13, b.ws.cpu())):
+        with pytest.raises(ValueError):
+            lf.lf_attn_bwd_mod(desc, mod, *args[:i], bad, *args[i + 1:])
