@@ -27,10 +27,17 @@ from . import (Buffers, lf_attn_bwd, lf_attn_bwd_mod, lf_attn_fwd, lf_attn_fwd_m
 _step_counter = itertools.count()
 
 
+def _score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start):
+    """The modifier of the scores, or None for the plain attention."""
+    if softcap or alibi_slopes is not None or prefix_len is not None or row_start is not None or prefix_causal:
+        return make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
+    return None
+
+
 class LazyFlashAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal, block_q,
-                softmax_scale, selection_out, mod):
+                softmax_scale, selection_out, softcap, alibi_slopes, prefix_len, prefix_causal, row_start):
         for t in (q, k, v):
             if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("q, k, v must be contiguous bf16 CUDA tensors")
@@ -41,6 +48,7 @@ class LazyFlashAttention(torch.autograd.Function):
         o = torch.empty_like(q)
         lse = torch.empty(hq, T, dtype=torch.float32, device=q.device)
         o_low = None
+        mod = _score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
         if mod is None:
             lf_attn_fwd(desc, q, k, v, o, lse)
         else:
@@ -48,8 +56,11 @@ class LazyFlashAttention(torch.autograd.Function):
             if any(ctx.needs_input_grad):
                 o_low = torch.empty_like(q)
             lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, o_low)
-        ctx.mod = mod
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low)
+        # the modifier's arrays are saved as cu_seqlens is, so that one written to between the two
+        # passes is noticed: P comes from this pass's LSE and the backward's own scores
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low, alibi_slopes, prefix_len, row_start)
+        ctx.softcap = softcap
+        ctx.prefix_causal = prefix_causal
         ctx.desc = desc
         ctx.delta = float(delta)
         ctx.seed = int(seed)
@@ -59,25 +70,26 @@ class LazyFlashAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_o):
-        q, k, v, o, lse, cu_seqlens, o_low = ctx.saved_tensors
+        q, k, v, o, lse, cu_seqlens, o_low, alibi_slopes, prefix_len, row_start = ctx.saved_tensors
         desc = ctx.desc
+        mod = _score_mod(ctx.softcap, alibi_slopes, prefix_len, ctx.prefix_causal, row_start)
         dout = grad_o.to(torch.bfloat16).contiguous()
         # the backward's own buffers only: o and lse are the forward's saved tensors
         bufs = Buffers(desc, device=q.device, forward=False)
         # with modified scores the backward computes D itself, from o and its residual
-        D = bufs.D if ctx.mod is None else None
+        D = bufs.D if mod is None else None
         lf_block_select(desc, dout, o, ctx.delta, ctx.seed, ctx.step, 0, bufs.norm, D,
                         bufs.tau, bufs.w, bufs.keep, bufs.kept_idx, bufs.kept_cnt)
         args = (q, k, v, o, lse, dout, D, bufs.w, bufs.kept_idx, bufs.kept_cnt, bufs.dq, bufs.dk,
                 bufs.dv, bufs.ws)
-        if ctx.mod is None:
+        if mod is None:
             lf_attn_bwd(desc, *args)
         else:
-            lf_attn_bwd_mod(desc, ctx.mod, *args, o_low)
+            lf_attn_bwd_mod(desc, mod, *args, o_low)
         if ctx.selection_out is not None:
             ctx.selection_out.update(norm=bufs.norm, tau=bufs.tau, keep=bufs.keep,
                                      weight=bufs.w, kept_cnt=bufs.kept_cnt, step=ctx.step)
-        return (bufs.dq, bufs.dk, bufs.dv) + (None,) * 10
+        return (bufs.dq, bufs.dk, bufs.dv) + (None,) * 14
 
 
 def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step=None,
@@ -98,11 +110,9 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's."""
     if alibi_slopes is not None and alibi_slopes.requires_grad:
         raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
-    mod = None
-    if softcap or alibi_slopes is not None or prefix_len is not None or row_start is not None or prefix_causal:
-        mod = make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
-                                    block_q, softmax_scale, selection_out, mod)
+                                    block_q, softmax_scale, selection_out, softcap, alibi_slopes, prefix_len,
+                                    prefix_causal, row_start)
 
 
 class QkNormRope(torch.autograd.Function):
