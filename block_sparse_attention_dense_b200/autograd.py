@@ -76,6 +76,9 @@ class LazyFlashAttention(torch.autograd.Function):
         dout = grad_o.to(torch.bfloat16).contiguous()
         # the backward's own buffers only: o and lse are the forward's saved tensors
         bufs = Buffers(desc, device=q.device, forward=False)
+        if desc.max_seqlen == 0:   # an empty batch: the selection writes nothing
+            bufs.tau.zero_()
+            bufs.kept_cnt.zero_()
         # with modified scores the backward computes D itself, from o and its residual
         D = bufs.D if mod is None else None
         lf_block_select(desc, dout, o, ctx.delta, ctx.seed, ctx.step, 0, bufs.norm, D,

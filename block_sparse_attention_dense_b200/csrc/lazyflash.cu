@@ -631,15 +631,16 @@ static lf_status block_select_impl(const lf_attn_desc* desc, const void* dout, c
     }
     if (flags & ~LF_SELECT_NORMS_GIVEN) return LF_ERR_INVALID_ARG;
     const bool norms_given = (flags & LF_SELECT_NORMS_GIVEN) != 0;
-    // dout is needed for the norms, o only for D
-    if ((!norms_given && !dout) || (D && (!dout || !o)) || !block_norm || !tau || !block_weight ||
-        !keep || !kept_idx || !kept_cnt)
+    // dout is needed for the norms, o only for D; empty tensors have no address
+    const bool rows = desc->total_tokens > 0, blocks = desc->max_seqlen > 0;
+    if ((rows && ((!norms_given && !dout) || (D && (!dout || !o)))) || !tau || !kept_cnt)
         return LF_ERR_INVALID_ARG;
+    if ((rows || blocks) && (!block_norm || !block_weight || !keep || !kept_idx)) return LF_ERR_INVALID_ARG;
     const void* ptrs[] = {dout, o, block_norm, D, tau, block_weight, keep, kept_idx, kept_cnt};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return LF_ERR_INVALID_ARG;
     if ((st = pending_device_error()) != LF_OK) return st;
-    if (desc->max_seqlen == 0) return LF_OK;
+    if (!blocks) return LF_OK;
     const int nbmax = nbmax_of(desc);
     if ((size_t)nbmax * sizeof(double) > 200 * 1024) return LF_ERR_UNSUPPORTED;
     if ((st = prepare_device()) != LF_OK) return st;

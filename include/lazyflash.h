@@ -130,7 +130,9 @@ lf_status lf_attn_fwd(const lf_attn_desc* desc, const void* q, const void* k, co
  *   delta must lie in [0, 1).  dout and o are [T][hq][d] bf16.  D may be NULL: the
  *   norm pass then reads dout only (o may be NULL as well), and lf_attn_bwd, given
  *   D = NULL, computes D itself for the rows of kept blocks.  With
- *   LF_SELECT_NORMS_GIVEN and D = NULL no norm pass runs (dout may be NULL). */
+ *   LF_SELECT_NORMS_GIVEN and D = NULL no norm pass runs (dout may be NULL).
+ *   With total_tokens = 0 dout, o and D may be NULL; with max_seqlen = 0 as well the
+ *   per-block arrays too (they have no elements), and nothing is written. */
 lf_status lf_block_select(const lf_attn_desc* desc, const void* dout, const void* o,
                           double delta, uint64_t seed, uint64_t step, uint32_t flags,
                           float* block_norm, float* D, double* tau, float* block_weight,

@@ -1,10 +1,22 @@
-"""Attention with modified scores through autograd: arrays changed between the two passes."""
-import pytest
+"""Attention with modified scores through autograd: arrays changed between the two passes,
+empty batches."""
+import ctypes
 
+import pytest
+import torch
+
+import block_sparse_attention_dense_b200 as lf
+from block_sparse_attention_dense_b200 import build as lfbuild
 from block_sparse_attention_dense_b200.autograd import lazyflash_attention
-from test_score_mods import NAMED, dev
+from test_score_mods import NAMED, dev, raw_desc
 
 gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    lfbuild.build()
+    return lf.lib()
 
 
 def attend(c, g, **kw):
@@ -25,3 +37,33 @@ def test_arrays_changed_between_the_passes_are_noticed(name):
     g[name].add_(0)   # the same values: what counts is that they were written
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         o.backward(g["dout"])
+
+
+@gpu
+@pytest.mark.parametrize("longest", [0, 200])
+def test_training_step_of_an_empty_batch(longest):
+    q, k, v = (torch.zeros(0, h, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True) for h in (4, 2, 2))
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    start = torch.zeros(0, dtype=torch.int32, device="cuda")
+    drawn = {}
+    o = lazyflash_attention(q, k, v, cu, longest, softcap=20.0, row_start=start, selection_out=drawn)
+    o.backward(torch.zeros_like(o))
+    lf.lf_sync_status()
+    assert o.shape == q.shape and all(x.grad is not None and x.grad.shape == x.shape for x in (q, k, v))
+    blocks = -(-longest // 128)
+    assert drawn["norm"].shape == (2, 4, blocks) and (drawn["kept_cnt"] == 0).all() and (drawn["tau"] == 0).all()
+
+
+def test_selection_of_no_rows_needs_no_token_tensors(L):
+    """As the forward and the backward with modified scores: empty tensors have no address."""
+    d = raw_desc(total_tokens=0, max_seqlen=0)
+    p = 0x10000
+    tail = [None, 0, None]
+    # dout, o | norm, D, tau, weight, keep, kept_idx, kept_cnt
+    assert L.lf_block_select(ctypes.byref(d), None, None, 0.1, 0, 0, 0, None, None, p, None, None, None, p, *tail) == 0
+    for missing in (2, 6):   # tau and kept_cnt have nseq * hq elements whatever the rows
+        outs = [None, None, p, None, None, None, p]
+        outs[missing] = None
+        assert L.lf_block_select(ctypes.byref(d), None, None, 0.1, 0, 0, 0, *outs, *tail) == lf.LF_ERR_INVALID_ARG
+    rows = raw_desc()
+    assert L.lf_block_select(ctypes.byref(rows), None, None, 0.1, 0, 0, 0, p, None, p, p, p, p, p, *tail) == lf.LF_ERR_INVALID_ARG
