@@ -37,7 +37,8 @@ def _score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start):
 class LazyFlashAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal, block_q,
-                softmax_scale, selection_out, softcap, alibi_slopes, prefix_len, prefix_causal, row_start):
+                softmax_scale, selection_out, softcap=0.0, alibi_slopes=None, prefix_len=None,
+                prefix_causal=False, row_start=None):
         for t in (q, k, v):
             if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("q, k, v must be contiguous bf16 CUDA tensors")

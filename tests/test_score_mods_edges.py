@@ -1,5 +1,5 @@
 """Attention with modified scores through autograd: arrays changed between the two passes,
-empty batches."""
+empty batches, the function's own arguments."""
 import ctypes
 
 import pytest
@@ -7,8 +7,8 @@ import torch
 
 import block_sparse_attention_dense_b200 as lf
 from block_sparse_attention_dense_b200 import build as lfbuild
-from block_sparse_attention_dense_b200.autograd import lazyflash_attention
-from test_score_mods import NAMED, dev, raw_desc
+from block_sparse_attention_dense_b200.autograd import LazyFlashAttention, lazyflash_attention
+from test_score_mods import NAMED, B, dev, raw_desc
 
 gpu = pytest.mark.gpu
 
@@ -67,3 +67,17 @@ def test_selection_of_no_rows_needs_no_token_tensors(L):
         assert L.lf_block_select(ctypes.byref(d), None, None, 0.1, 0, 0, 0, *outs, *tail) == lf.LF_ERR_INVALID_ARG
     rows = raw_desc()
     assert L.lf_block_select(ctypes.byref(rows), None, None, 0.1, 0, 0, 0, p, None, p, p, p, p, p, *tail) == lf.LF_ERR_INVALID_ARG
+
+
+@gpu
+def test_the_function_takes_the_arguments_of_the_plain_attention():
+    """LazyFlashAttention.apply without a modifier: twelve arguments, as for the plain attention."""
+    c = NAMED["cap"]
+    g = dev(c.make())
+    x = [[g[n].clone().requires_grad_(True) for n in ("q", "k", "v")] for _ in range(2)]
+    o = LazyFlashAttention.apply(*x[0], g["cu"], max(c.lens), 0.2, 3, 0, True, 128, None, None)
+    z = lazyflash_attention(*x[1], g["cu"], max(c.lens), delta=0.2, seed=3, step=0)
+    o.backward(g["dout"])
+    z.backward(g["dout"])
+    assert torch.equal(o, z) and torch.equal(x[0][1].grad, x[1][1].grad) and torch.equal(x[0][2].grad, x[1][2].grad)
+    assert (x[0][0].grad.float() - x[1][0].grad.float()).norm() <= B * x[1][0].grad.float().norm()
