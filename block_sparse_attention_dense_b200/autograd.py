@@ -112,7 +112,7 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     distance; no gradient), ``prefix_len`` [nseq], ``prefix_causal`` and ``row_start`` [T]
     (prefix, document, window and shared-prompt masks) modify the scores of both directions:
     lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's."""
-    if alibi_slopes is not None and alibi_slopes.requires_grad:
+    if alibi_slopes is not None and alibi_slopes.requires_grad and torch.is_grad_enabled():
         raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
                                     block_q, softmax_scale, selection_out, softcap, alibi_slopes, prefix_len,

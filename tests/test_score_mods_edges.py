@@ -1,5 +1,5 @@
 """Attention with modified scores through autograd: arrays changed between the two passes,
-empty batches, the function's own arguments."""
+empty batches, the function's own arguments, slopes that are parameters."""
 import ctypes
 
 import pytest
@@ -81,3 +81,19 @@ def test_the_function_takes_the_arguments_of_the_plain_attention():
     z.backward(g["dout"])
     assert torch.equal(o, z) and torch.equal(x[0][1].grad, x[1][1].grad) and torch.equal(x[0][2].grad, x[1][2].grad)
     assert (x[0][0].grad.float() - x[1][0].grad.float()).norm() <= B * x[1][0].grad.float().norm()
+
+
+def test_slopes_are_refused_only_where_a_gradient_is_recorded():
+    x, slopes = torch.zeros(4, 2, 64), torch.zeros(2, requires_grad=True)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # only the device is wrong
+        lazyflash_attention(x, x, x, torch.tensor([0, 4]), 4, alibi_slopes=slopes)
+
+
+@gpu
+def test_slopes_that_are_a_parameter_without_grad():
+    c = NAMED["everything"]
+    g = dev(c.make())
+    want = attend(c, g)
+    with torch.no_grad():
+        got = attend(c, dict(g, slopes=torch.nn.Parameter(g["slopes"])))
+    assert torch.equal(got, want)
