@@ -166,5 +166,7 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos_sin=None, cu_seqlens=No
     (contiguous heads, any token stride).  The results are contiguous and go into
     lazyflash_attention.  cos_sin: rope_cos_sin(npos, rot), or None for the norm alone;
     norm=False rotates only.  A row's position is its index in its segment of cu_seqlens,
-    or positions[row]."""
+    or positions[row].  No gradient is computed for the table."""
+    if cos_sin is not None and cos_sin.requires_grad and torch.is_grad_enabled():
+        raise ValueError("no gradient is computed for cos_sin: pass it detached")
     return QkNormRope.apply(q, k, q_weight, k_weight, cos_sin, cu_seqlens, positions, eps, norm, interleaved)

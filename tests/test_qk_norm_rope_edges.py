@@ -1,5 +1,5 @@
-"""Head norms with rotation: eps = 0 with lanes and rows that hold nothing.  References and
-tolerances are those of test_qk_norm_rope.py."""
+"""Head norms with rotation: eps = 0 with lanes and rows that hold nothing, and tables that
+ask for a gradient.  References and tolerances are those of test_qk_norm_rope.py."""
 import pytest
 import torch
 
@@ -49,3 +49,13 @@ def test_weight_gradients_without_eps(c):
     torch.autograd.backward(y, (g["dyq"], g["dyk"]))
     for w, dw in zip(weights, (dqw, dkw)):
         assert torch.equal(w.grad, dw.to(w.dtype))
+
+
+def test_a_table_that_asks_for_a_gradient_is_refused():
+    q, k = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    table = lf.rope_cos_sin(8, 64, device="cpu").requires_grad_(True)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="cos_sin"):
+        qk_norm_rope(q, k, None, None, table, cu)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # no gradient is asked for: only the device is wrong
+        qk_norm_rope(q, k, None, None, table, cu)
