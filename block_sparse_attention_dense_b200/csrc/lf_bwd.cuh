@@ -677,12 +677,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                                            __uint_as_float(dr[4 * e4 + u + 1]));
                             float2 x, damp;
                             if constexpr (kCap) {
-                                const float2 y = kGeneral ? cap_any(*mod_of(prm), s2)
-                                                          : f2_mul(s2, cap_fused_factor(*mod_of(prm), s2));
+                                float2 y;
+                                if constexpr (kGeneral) {
+                                    y = cap_any(*mod_of(prm), s2, damp);
+                                } else {
+                                    y = f2_mul(s2, cap_fused_factor(*mod_of(prm), s2));
+                                    // 1 - tanh^2
+                                    const float dc = mod_of(prm)->cap_damp;
+                                    damp = f2_fma(f2_mul(y, y), make_float2(dc, dc), make_float2(1.f, 1.f));
+                                }
                                 x = f2_add(y, nl);
-                                // 1 - tanh^2
-                                const float dc = mod_of(prm)->cap_damp;
-                                damp = f2_fma(f2_mul(y, y), make_float2(dc, dc), make_float2(1.f, 1.f));
                             } else {
                                 x = f2_fma(s2, sc2, nl);
                             }

@@ -89,6 +89,19 @@ __device__ __forceinline__ float2 cap_any(const ModParams& m, float2 s) {
                        fabsf(s.y * m.cap_in) <= kCapRange ? y.y : cap_far(m, s.y));
 }
 
+// The same with the derivative 1 - tanh^2.  It comes from r = 2 / (1 + exp(2 |x|)), as
+// |tanh x| = 1 - r: the derivative is r (2 - r), to a few roundings of itself at every x.  From
+// y it would be off by y's own rounding, about 1e-6, which is more than all of it for |x| above 7.
+__device__ __forceinline__ float2 cap_any(const ModParams& m, float2 s, float2& damp) {
+    const float2 x = f2_mul(s, make_float2(m.cap_in, m.cap_in)), y = cap_near(m, s);
+    auto ratio = [](float v) { return __fdividef(2.f, 1.f + fast_exp2(fabsf(v) * 2.8853900817779268f)); };
+    const float2 r = make_float2(ratio(x.x), ratio(x.y));
+    damp = f2_mul(r, f2_sub(make_float2(2.f, 2.f), r));
+    const float2 far = f2_fma(make_float2(-m.cap_out, -m.cap_out), r, make_float2(m.cap_out, m.cap_out));
+    return make_float2(fabsf(x.x) <= kCapRange ? y.x : copysignf(far.x, x.x),
+                       fabsf(x.y) <= kCapRange ? y.y : copysignf(far.y, x.y));
+}
+
 // The largest value, and the largest size, of a thread's 128 scores (three-input maxima,
 // four independent chains).
 __device__ __forceinline__ float row_max(const float (&s)[128]) {

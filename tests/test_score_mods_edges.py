@@ -1,6 +1,8 @@
 """Attention with modified scores through autograd: arrays changed between the two passes,
-empty batches, the function's own arguments, slopes that are parameters."""
+empty batches, the function's own arguments, slopes that are parameters;
+and rows whose scores all lie where the cap is flat."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -8,7 +10,7 @@ import torch
 import block_sparse_attention_dense_b200 as lf
 from block_sparse_attention_dense_b200 import build as lfbuild
 from block_sparse_attention_dense_b200.autograd import LazyFlashAttention, lazyflash_attention
-from test_score_mods import NAMED, B, dev, raw_desc
+from test_score_mods import NAMED, B, U, dev, raw_desc
 
 gpu = pytest.mark.gpu
 
@@ -97,3 +99,60 @@ def test_slopes_that_are_a_parameter_without_grad():
     with torch.no_grad():
         got = attend(c, dict(g, slopes=torch.nn.Parameter(g["slopes"])))
     assert torch.equal(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("d,block,prefix", [(128, 128, None), (64, 64, 40)])
+def test_rows_whose_scores_are_all_saturated(d, block, prefix):
+    """|x| / cap between 7 and 12 for every score, where 1 - tanh^2 = 4 e / (1 + e)^2, e = exp(2 |x| / cap),
+    is 3e-6 to 1e-10: the gradient is that small, and right.
+
+    Off by (u = 2^-24, b = 2^-8): x by d u scale sum|q_i k_i| + 4 u |x| (ex), which changes the
+    derivative by 2 ex / cap of itself and every z by less than 1e-6 cap (tanh as computed), P
+    by twice that and 1e-6 (ep); the derivative's own operations (two roundings of an exponent
+    below 40, exp2, a sum, a reciprocal, a product) by 2 * 40 u + 16 u of itself.  D, dP and
+    the sums as in test_score_mods.py."""
+    n, hq, hkv, cap, scale = 300, 2, 1, 1.0, 1.0 / math.sqrt(d)
+    gen = torch.Generator().manual_seed(0)
+    axis = torch.randn(d, generator=gen).sign()
+    # q = s axis + noise, k = axis + noise: x = +-(7 to 12)
+    size = 8.0 + 3.0 * torch.rand(n, hq, 1, generator=gen)
+    sign = torch.randn(n, hq, 1, generator=gen).sign()
+    q = (sign * size / math.sqrt(d) * axis + 0.02 * torch.randn(n, hq, d, generator=gen)).bfloat16()
+    k = (axis + 0.02 * torch.randn(n, hkv, d, generator=gen)).bfloat16()
+    v, do = (torch.randn(n, h, d, generator=gen).bfloat16() for h in (hkv, hq))
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    leaves = [t.cuda().requires_grad_(True) for t in (q, k, v)]
+    plen = None if prefix is None else torch.tensor([prefix], dtype=torch.int32, device="cuda")
+    o = lazyflash_attention(*leaves, cu, n, delta=0.0, block_q=block, softcap=cap, softmax_scale=scale, prefix_len=plen)
+    o.backward(do.cuda())
+    lf.lf_sync_status()
+    see = torch.ones(n, n).tril().bool()
+    if prefix is not None:
+        see[:, :prefix] = True
+    kd, vd = k[:, 0].double(), v[:, 0].double()
+    dk, tk = torch.zeros(n, d, dtype=torch.float64), torch.zeros(n, d, dtype=torch.float64)
+    for h in range(hq):
+        qd, dod = q[:, h].double(), do[:, h].double()
+        x = qd @ kd.T * scale
+        assert x.abs().min() > 7 * cap and x.abs().max() < 12 * cap
+        ex = d * U * scale * (qd.abs() @ kd.abs().T) + 4 * U * x.abs()
+        p = torch.softmax((cap * torch.tanh(x / cap)).masked_fill(~see, -math.inf), 1)
+        ep = 2 * (1e-6 * cap) + 1e-6
+        e = torch.exp(2 * x.abs() / cap)
+        damp = 4 * e / (1 + e).square()
+        edamp = 2 * ex / cap + (2 * 40 + 16) * U
+        out = p @ vd
+        dp, D = dod @ vd.T, (dod * out).sum(1, keepdim=True)
+        ds = p * (dp - D) * damp
+        edp = d * U * (dod.abs() @ vd.abs().T)
+        eD = 2 * (B + ep) * (p * (dp - D).abs()).sum(1, keepdim=True) + edp.amax(1, keepdim=True)
+        eD += (B * B + d * U) * (dod.abs() * out.abs()).sum(1, keepdim=True)
+        eds = (B + ep + edamp + 4 * U) * ds.abs() + p * damp * (eD + edp) + n * hq * U * ds.abs()
+        want, tol = scale * ds @ kd, scale * eds @ kd.abs()
+        got = leaves[0].grad[:, h].double().cpu()
+        assert ((got - want).abs() <= tol + B * want.abs()).all(), float(((got - want).abs() / (tol + B * want.abs())).max())
+        dk += scale * ds.T @ qd
+        tk += scale * eds.T @ qd.abs()
+    got = leaves[1].grad[:, 0].double().cpu()
+    assert ((got - dk).abs() <= tk + B * dk.abs()).all(), float(((got - dk).abs() / (tk + B * dk.abs())).max())
