@@ -60,6 +60,7 @@ class lf_score_mod(ctypes.Structure):
         ("prefix_len", ctypes.c_void_p),
         ("prefix_causal", ctypes.c_int32),
         ("row_start", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
     ]
 
 
@@ -309,19 +310,19 @@ def _vector(t, name, device, dtypes, numel=None):
 # attention with modified scores
 # --------------------------------------------------------------------------------------
 def make_score_mod(softcap: float = 0.0, alibi_slopes=None, prefix_len=None, prefix_causal: bool = False,
-                   row_start=None) -> lf_score_mod:
+                   row_start=None, positions=None) -> lf_score_mod:
     """Modifier of lf_attn_fwd_mod and lf_attn_bwd_mod (meaning: include/lazyflash.h).
-    alibi_slopes fp32 [hq], prefix_len int32 [nseq], row_start int32 [T]: CUDA tensors on
-    one device, which the modifier keeps."""
-    given = [t for t in (alibi_slopes, prefix_len, row_start) if t is not None]
+    alibi_slopes fp32 [hq], prefix_len int32 [nseq], row_start and positions int32 [T]: CUDA
+    tensors on one device, which the modifier keeps."""
+    given = [t for t in (alibi_slopes, prefix_len, row_start, positions) if t is not None]
     dev = given[0].device if given else None
     if dev is not None and dev.type != "cuda":
         raise ValueError("the modifier's arrays must be CUDA tensors")
     i32 = (torch.int32,)
     mod = lf_score_mod(float(softcap), _vector(alibi_slopes, "alibi_slopes", dev, (torch.float32,)),
                        _vector(prefix_len, "prefix_len", dev, i32), int(bool(prefix_causal)),
-                       _vector(row_start, "row_start", dev, i32))
-    mod._keepalive = (alibi_slopes, prefix_len, row_start)
+                       _vector(row_start, "row_start", dev, i32), _vector(positions, "positions", dev, i32))
+    mod._keepalive = (alibi_slopes, prefix_len, row_start, positions)
     mod._sizes = tuple(None if t is None else t.numel() for t in mod._keepalive)
     mod._device = dev
     return mod
@@ -343,7 +344,8 @@ def _check_attention(desc, mod, q, k, v, rest=()):
     keep = getattr(desc, "_keepalive", None)
     if (keep is not None and keep.device != dev) or (mod._device is not None and mod._device != dev):
         raise ValueError("cu_seqlens and the modifier's arrays must be on %s" % dev)
-    for name, n, want in zip(("alibi_slopes", "prefix_len", "row_start"), mod._sizes, (desc.hq, desc.nseq, T)):
+    for name, n, want in zip(("alibi_slopes", "prefix_len", "row_start", "positions"), mod._sizes,
+                             (desc.hq, desc.nseq, T, T)):
         if n is not None and n != want:
             raise ValueError("%s must have %d elements, not %d" % (name, want, n))
     return dev
@@ -382,7 +384,8 @@ def shared_prompt_tables(prompt_lens, answer_lens, device="cuda"):
     prompt (prompt_lens[s] tokens) followed by its answers (answer_lens[s], a list of
     lengths).  Returns (cu_seqlens, prefix_len, row_start, positions), int32: the mask's
     arrays for make_score_mod(prefix_len=..., prefix_causal=True, row_start=...), and each
-    token's position, every answer's continuing its prompt's, for qk_norm_rope."""
+    token's position, every answer's continuing its prompt's, for qk_norm_rope and, where the
+    scores have a distance bias, for make_score_mod(positions=...)."""
     cu, start, pos = [0], [], []
     for p, answers in zip(prompt_lens, answer_lens, strict=True):
         at = int(p)

@@ -27,10 +27,12 @@ from . import (Buffers, lf_attn_bwd, lf_attn_bwd_mod, lf_attn_fwd, lf_attn_fwd_m
 _step_counter = itertools.count()
 
 
-def _score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start):
-    """The modifier of the scores, or None for the plain attention."""
-    if softcap or alibi_slopes is not None or prefix_len is not None or row_start is not None or prefix_causal:
-        return make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
+def _score_mod(softcap, prefix_causal, *arrays):
+    """The modifier of the scores, or None for the plain attention; arrays: alibi_slopes,
+    prefix_len, row_start, positions."""
+    if softcap or prefix_causal or any(a is not None for a in arrays):
+        alibi_slopes, prefix_len, row_start, positions = arrays
+        return make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions)
     return None
 
 
@@ -38,7 +40,7 @@ class LazyFlashAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal, block_q,
                 softmax_scale, selection_out, softcap=0.0, alibi_slopes=None, prefix_len=None,
-                prefix_causal=False, row_start=None):
+                prefix_causal=False, row_start=None, positions=None):
         for t in (q, k, v):
             if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("q, k, v must be contiguous bf16 CUDA tensors")
@@ -49,7 +51,8 @@ class LazyFlashAttention(torch.autograd.Function):
         o = torch.empty_like(q)
         lse = torch.empty(hq, T, dtype=torch.float32, device=q.device)
         o_low = None
-        mod = _score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start)
+        arrays = (alibi_slopes, prefix_len, row_start, positions)
+        mod = _score_mod(softcap, prefix_causal, *arrays)
         if mod is None:
             lf_attn_fwd(desc, q, k, v, o, lse)
         else:
@@ -59,7 +62,7 @@ class LazyFlashAttention(torch.autograd.Function):
             lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, o_low)
         # the modifier's arrays are saved as cu_seqlens is, so that one written to between the two
         # passes is noticed: P comes from this pass's LSE and the backward's own scores
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low, alibi_slopes, prefix_len, row_start)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low, *arrays)
         ctx.softcap = softcap
         ctx.prefix_causal = prefix_causal
         ctx.desc = desc
@@ -71,9 +74,9 @@ class LazyFlashAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_o):
-        q, k, v, o, lse, cu_seqlens, o_low, alibi_slopes, prefix_len, row_start = ctx.saved_tensors
+        q, k, v, o, lse, cu_seqlens, o_low, *arrays = ctx.saved_tensors
         desc = ctx.desc
-        mod = _score_mod(ctx.softcap, alibi_slopes, prefix_len, ctx.prefix_causal, row_start)
+        mod = _score_mod(ctx.softcap, ctx.prefix_causal, *arrays)
         dout = grad_o.to(torch.bfloat16).contiguous()
         # the backward's own buffers only: o and lse are the forward's saved tensors
         bufs = Buffers(desc, device=q.device, forward=False)
@@ -93,13 +96,13 @@ class LazyFlashAttention(torch.autograd.Function):
         if ctx.selection_out is not None:
             ctx.selection_out.update(norm=bufs.norm, tau=bufs.tau, keep=bufs.keep,
                                      weight=bufs.w, kept_cnt=bufs.kept_cnt, step=ctx.step)
-        return (bufs.dq, bufs.dk, bufs.dv) + (None,) * 14
+        return (bufs.dq, bufs.dk, bufs.dv) + (None,) * 15
 
 
 def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step=None,
                         causal=True, block_q=128, softmax_scale=None, selection_out=None,
                         softcap=0.0, alibi_slopes=None, prefix_len=None, prefix_causal=False,
-                        row_start=None):
+                        row_start=None, positions=None):
     """Dense attention forward, LazyFlash block-sparse backward.
 
     ``step`` defaults to a process-wide counter, so every backward draws a
@@ -111,12 +114,15 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     ``softcap`` (scores capped by a tanh), ``alibi_slopes`` [hq] (a bias that falls with the
     distance; no gradient), ``prefix_len`` [nseq], ``prefix_causal`` and ``row_start`` [T]
     (prefix, document, window and shared-prompt masks) modify the scores of both directions:
-    lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's."""
+    lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's.  The
+    bias counts rows of the packed segment: answers that share a prompt need ``positions`` [T]
+    (the table's fourth) as well, from which it then counts the distance to the prompt's keys;
+    without, an answer is too far from its prompt by the answers packed before it."""
     if alibi_slopes is not None and alibi_slopes.requires_grad and torch.is_grad_enabled():
         raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
                                     block_q, softmax_scale, selection_out, softcap, alibi_slopes, prefix_len,
-                                    prefix_causal, row_start)
+                                    prefix_causal, row_start, positions)
 
 
 class QkNormRope(torch.autograd.Function):

@@ -125,10 +125,12 @@ lf_status check_mod(const lf_attn_desc* d, const lf_score_mod* m) {
     if (m->softcap != 0.f && !(m->softcap >= 1e-3f && m->softcap <= 1e6f)) return LF_ERR_INVALID_ARG;
     // read value by value: slices of longer arrays are fine
     for (const void* p : {static_cast<const void*>(m->alibi_slopes), static_cast<const void*>(m->prefix_len),
-                          static_cast<const void*>(m->row_start)})
+                          static_cast<const void*>(m->row_start), static_cast<const void*>(m->positions)})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return LF_ERR_INVALID_ARG;
     if (m->prefix_causal != 0 && m->prefix_causal != 1) return LF_ERR_INVALID_ARG;
     if (m->prefix_causal && !m->prefix_len) return LF_ERR_INVALID_ARG;
+    if (m->positions && !m->prefix_len) return LF_ERR_INVALID_ARG;
+    if (m->positions && !m->prefix_causal) return LF_ERR_UNSUPPORTED;   // a prefix's own rows see later keys
     // the masks say which keys a causal row sees besides, or no longer
     if ((m->prefix_len || m->row_start) && !d->causal) return LF_ERR_UNSUPPORTED;
     return LF_OK;
@@ -137,7 +139,8 @@ lf_status check_mod(const lf_attn_desc* d, const lf_score_mod* m) {
 // The kernels' variant for a modifier, and its parameters.
 int mod_variant(const lf_score_mod* m) {
     return !m ? 0 : (m->softcap != 0.f ? lf::kModCap : 0) | (m->alibi_slopes ? lf::kModBias : 0) |
-                        (m->prefix_len || m->row_start ? lf::kModMask : 0);
+                        (m->prefix_len || m->row_start ? lf::kModMask : 0) |
+                        (m->alibi_slopes && m->positions ? lf::kModPositions : 0);
 }
 lf::ModParams mod_params(const lf_attn_desc* d, const lf_score_mod* m) {
     lf::ModParams p{};
@@ -184,6 +187,7 @@ lf_status launch_fwd(const lf_attn_desc* d, const lf_score_mod* mod, const void*
         p.mod = mod_params(d, mod);
         p.o_low = static_cast<__nv_bfloat16*>(o_low);
     }
+    if constexpr ((kMod & lf::kModPositions) != 0) p.positions = mod->positions;
     const uint32_t smem = lf::FwdSmem<D>::kAlloc;
     if (cudaFuncSetAttribute(lf::attn_fwd_kernel<D, kMod>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
@@ -303,7 +307,9 @@ lf_status launch_bwd(const lf_attn_desc* d, const lf_score_mod* mod, int32_t* ke
         p.mod = mod_params(d, mod);
         p.key_last = key_last;
     }
-    const uint32_t smem = lf::BwdSmem<D>::kAlloc;
+    if constexpr ((kMod & lf::kModPositions) != 0) p.positions = mod->positions;
+    const uint32_t smem =
+        (kMod & lf::kModPositions) != 0 ? lf::BwdSmem<D>::kAllocPositions : lf::BwdSmem<D>::kAlloc;
     // 64-row selection blocks: the variant that skips a tile's dropped half
     auto kern = d->block_q == 64 ? lf::attn_bwd_kernel<D, true, kMod> : lf::attn_bwd_kernel<D, false, kMod>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -348,7 +354,9 @@ lf_status by_variant(const lf_attn_desc* d, const lf_score_mod* mod, F&& f) {
         case 4: return by_d(std::integral_constant<int, 4>{});
         case 5: return by_d(std::integral_constant<int, 5>{});
         case 6: return by_d(std::integral_constant<int, 6>{});
-        default: return by_d(std::integral_constant<int, 7>{});
+        case 7: return by_d(std::integral_constant<int, 7>{});
+        case 14: return by_d(std::integral_constant<int, 14>{});   // positions come with bias and mask
+        default: return by_d(std::integral_constant<int, 15>{});
     }
 }
 lf_status launch_fwd_any(const lf_attn_desc* d, const lf_score_mod* mod, const void* q, const void* k,

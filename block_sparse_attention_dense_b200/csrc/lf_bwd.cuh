@@ -93,8 +93,13 @@ struct BwdModParams : BwdParams {
 };
 __device__ __forceinline__ const ModParams* mod_of(const BwdParams&) { return nullptr; }
 __device__ __forceinline__ const ModParams* mod_of(const BwdModParams& p) { return &p.mod; }
+struct BwdPositionsParams : BwdModParams {
+    const int32_t* positions;  // [T] where distances to prefix keys are counted from
+};
 template <int kMod>
-using BwdParamsOf = std::conditional_t<kMod == 0, BwdParams, BwdModParams>;
+using BwdParamsOf =
+    std::conditional_t<kMod == 0, BwdParams,
+                       std::conditional_t<(kMod & kModPositions) != 0, BwdPositionsParams, BwdModParams>>;
 
 constexpr uint32_t kAccBox = 128 * 32 * 4;   // one staged 32-column fp32 box of a KV tile
 constexpr int kMaxHeadsPerCta = 32;           // query heads one backward CTA can walk
@@ -114,6 +119,11 @@ struct BwdSmem {
     static constexpr uint32_t kSlopes = kHeads + kMaxHeadsPerCta * 8;   // float per query head
     static constexpr uint32_t kBytes = kSlopes + kMaxHeadsPerCta * 4;
     static constexpr uint32_t kAlloc = kBytes + 1024;
+    // distances counted from positions: lse2 for prefix keys [128] in the slopes' place (which
+    // are then read from global memory), as a 128-wide head leaves no more room
+    static constexpr uint32_t kPrefixVec = kSlopes;
+    static constexpr uint32_t kAllocPositions = kPrefixVec + 128 * 4 + 1024;
+    static_assert(kAlloc <= 232448 && kAllocPositions <= 232448, "227 KB of shared memory per CTA");
 };
 
 constexpr int kBwdThreads = 512;
@@ -242,7 +252,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __grid_constant__ CUtensorMap tm_q64, const __grid_constant__ CUtensorMap tm_do64,
                     BwdParamsOf<kMod> prm) {
     using L = BwdSmem<D>;
-    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
+    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0,
+                   kPositions = (kMod & kModPositions) != 0;
     static_assert(2 * (D / 32) * kAccBox <= 4 * L::kTile, "dK/dV staging must fit the Q/dO buffers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool has = find_head_starts<kMask>(prm, prm.heads_per_cta, hgrp, s, jt, len, head_starts, first_row, last_row);
     float* slopes_s = reinterpret_cast<float*>(smem + L::kSlopes);   // -slope log2(e) per query head
     if constexpr (kBias) {
-        if (tid < prm.heads_per_cta)
+        if (!kPositions && tid < prm.heads_per_cta)
             slopes_s[tid] = prm.mod.slopes[hgrp * prm.heads_per_cta + tid] * -1.4426950408889634f;
     }
     tc_fence_before();
@@ -578,6 +589,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 q_last = prm.key_last[seg0 + kv_local];
             }
         }
+        // keys whose distances are counted from the rows' positions: their columns' part of the bias
+        // lies in a vector of its own, counted from the KV tile's first key, so that both parts
+        // stay of the distance's size
+        [[maybe_unused]] bool from_position = false;
+        [[maybe_unused]] float* prefix_s = reinterpret_cast<float*>(smem + L::kPrefixVec);
+        [[maybe_unused]] const float* cols_s = lse2_s;
+        if constexpr (kPositions) {
+            from_position = kv_valid && kv_local < P;
+            if (from_position) cols_s = prefix_s;
+        }
         int n = 0;
         // parity of each half's live pairs processed (bit hf: the half's barrier phase);
         // bits of one register rather than an array indexed by the half loop, which would
@@ -609,9 +630,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int qt = e.tile, q0 = qt * 128;
             // the bias per key of distance (log2 units), and the sign of query - key: one sign
             // over the tile pair, except on the diagonal where rows see later keys too
-            [[maybe_unused]] const float bias2 = kBias ? slopes_s[e.h - hgrp * prm.heads_per_cta] : 0.f;
+            [[maybe_unused]] float bias2 = 0.f;
+            if constexpr (kPositions)
+                bias2 = prm.mod.slopes[e.h] * -1.4426950408889634f;
+            else if constexpr (kBias)
+                bias2 = slopes_s[e.h - hgrp * prm.heads_per_cta];
             [[maybe_unused]] const float dist_sign = qt < jt ? -1.f : 1.f;
             const bool dist_both = kBias && two_sided && qt == jt;
+            [[maybe_unused]] const int q_from = kPositions && from_position ? jt * 128 : q0;
             if (r < 64) {
                 // this warpgroup's 64 columns: [32 wg, 32 wg + 32) of each half
                 const int col = (r >> 5) * 64 + wg * 32 + (r & 31);
@@ -624,6 +650,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
                 lse2_s[col] = -l2;   // stored negated: the exponent is one packed FMA
                 if constexpr (kBias) lse2_s[col] = fmaf(dist_sign * bias2, static_cast<float>(col), -l2);
+                if constexpr (kPositions) {   // rows see no later key: the sign is +
+                    const int row = min(q_local, len - 1);
+                    const int pos = bounded_position(prm.positions[seg0 + row], row, P);
+                    prefix_s[col] = fmaf(bias2, static_cast<float>(pos - jt * 128), -l2);
+                }
                 dvec_s[col] = dd;
             }
             named_bar_sync(2, 256);
@@ -654,14 +685,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 // the half's variant (warp-uniform): kWhole, every key of the warp sees every
                 // column, so nothing is compared (kMod only; the plain kernel always compares);
                 // kGeneral, capped scores outside the narrow fit, or distances of both signs
-                [[maybe_unused]] const float bias_u = kBias ? dist_sign * bias2 * static_cast<float>(q0 - kv_local) : 0.f;
+                [[maybe_unused]] const float bias_u = kBias ? dist_sign * bias2 * static_cast<float>(q_from - kv_local) : 0.f;
                 auto chunk = [&](int c, const uint32_t (&sr)[16], const uint32_t (&dr)[16], auto variant) {
                     constexpr bool kWhole = decltype(variant)::value == 1, kGeneral = decltype(variant)::value == 2;
                     uint32_t pk[8], dk_[8];
 #pragma unroll
                     for (int e4 = 0; e4 < 4; ++e4) {
                         const int col0 = hf * 64 + c * 16 + 4 * e4;
-                        const float4 l4 = *reinterpret_cast<const float4*>(lse2_s + col0);
+                        const float4 l4 = *reinterpret_cast<const float4*>((kPositions ? cols_s : lse2_s) + col0);
                         const float4 d4 = *reinterpret_cast<const float4*>(dvec_s + col0);
                         const float2 sc2 = make_float2(prm.scale_log2, prm.scale_log2);
                         const float2 w2 = make_float2(w, w);

@@ -29,7 +29,11 @@
 // Under a mask the two query tiles of a CTA share one list of KV tiles (the prefix's, and a
 // run up to the diagonal), and a tile that has nothing in a step only hands the step's
 // stages back, so that a document's end between the two does not make the later one walk
-// the earlier one's keys.  A row's softmax warp is bound by its own latency (the exp2 unit
+// the earlier one's keys.  Distances to prefix keys may be counted from the rows' positions
+// (kModPositions: a shared prompt's answers): a row's distances then have another start in the
+// prefix's tiles, and in the one tile at the prefix's end a start per key.  A variant of its
+// own, as the same code behind a runtime test made the biased masks 2-3 % slower.
+// A row's softmax warp is bound by its own latency (the exp2 unit
 // and the FMA pipes are busy 45 and 36 % of the time under a cap), so the cap and the bias
 // are laid beside the exp2 (capped_row; `fused`).  16,384 tokens, 32/8 heads of 128, causal,
 // plain 1.72 ms: cap 2.36, bias 1.86, a mask that hides nothing 1.87, both cap and bias
@@ -56,8 +60,13 @@ struct FwdModParams : FwdParams {
     ModParams mod;
     __nv_bfloat16* o_low;      // [T][hq][D] what rounding took from o, or null
 };
+struct FwdPositionsParams : FwdModParams {
+    const int32_t* positions;  // [T] where distances to prefix keys are counted from
+};
 template <int kMod>
-using FwdParamsOf = std::conditional_t<kMod == 0, FwdParams, FwdModParams>;
+using FwdParamsOf =
+    std::conditional_t<kMod == 0, FwdParams,
+                       std::conditional_t<(kMod & kModPositions) != 0, FwdPositionsParams, FwdModParams>>;
 
 template <int D>
 struct FwdSmem {
@@ -229,7 +238,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, FwdParamsOf<kMod> prm) {
     using L = FwdSmem<D>;
-    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0;
+    constexpr bool kCap = (kMod & kModCap) != 0, kBias = (kMod & kModBias) != 0, kMask = (kMod & kModMask) != 0,
+                   kPositions = (kMod & kModPositions) != 0;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -510,6 +520,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 all_from = min(max(rs[min(qt * 128 + 127, len - 1)], 0), len - 1);
             }
         }
+        // the row's index as its distances to prefix keys see it
+        [[maybe_unused]] auto q_prefix = [&](bool check) {
+            if constexpr (kPositions) {
+                const int row = min(q_local, len - 1), given = prm.positions[seg0 + row];
+                const int pos = bounded_position(given, row, P);
+                if (check && pos != given) {
+                    report_error(16, kErrBadMask);
+                    mirror_error();
+                }
+                return pos + (q_local - row);
+            } else {
+                return q_local;
+            }
+        };
+        if (kPositions && nk > 0) q_prefix(true);
         float bias2 = 0.f;   // per key of distance, in log2 units
         bool two_sided = false;
         if constexpr (kBias) {
@@ -534,6 +559,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // order, under a mask those of its two runs
         for (int j = !kMod ? 0 : kMask && nk > 0 ? max(runs.np, runs.hi) - 1 : nk - 1; kMod ? j >= 0 : j < nk;
              j = kMask ? runs.next(j) : kMod ? j - 1 : j + 1) {
+            // where the tile's distances are counted from (read anew for each tile: a register
+            // held across the steps spilled); at the prefix's end that holds for its keys below P
+            int q_dist = q_local;
+            bool prefix_end = false;
+            if (kPositions && j * 128 < P) {
+                q_dist = q_prefix(false);
+                prefix_end = j * 128 + 128 > P;
+            }
             const bool got = mbar_wait_or_abort(&bar_s_full[t], ka & 1, 30, abort_flag);
             if (!__all_sync(0xffffffffu, got)) { failed = true; break; }
             tc_fence_after();
@@ -553,10 +586,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 view.own = min(q_local, len - 1);
             }
             if constexpr (kCap) {
-                if (bounded && !(kBias && two_sided && j >= qt)) {
+                if (bounded && !(kBias && two_sided && j >= qt) && !prefix_end) {
                     // a tile under a cap: no maximum, no reference, and so the row is taken in
                     // chunks of 32 columns as they arrive
-                    const float dist_bias = static_cast<float>(q_local - kv0) * bias2;
+                    const float dist_bias = static_cast<float>(q_dist - kv0) * bias2;
                     const RowSums sums =
                         whole ? capped_row<kBias, false>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t])
                               : capped_row<kBias, true>(prm.mod, t_s, dist_bias, bias2, bias_in8, view, &bar_p_half[t]);
@@ -590,8 +623,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // reference: P <= 2^kFusedAbove is as exact as P <= 1
             bool fused = false;
             if constexpr (kBias && !kCap) {
-                if (whole && !(two_sided && j >= qt) && ka > 0) {
-                    const float nearest = static_cast<float>(q_local - kv0 - (bias2 <= 0.f ? 127 : 0));
+                if (whole && !(two_sided && j >= qt) && !prefix_end && ka > 0) {
+                    const float nearest = static_cast<float>(q_dist - kv0 - (bias2 <= 0.f ? 127 : 0));
                     const float bound = fmaf(nearest, bias2, row_max(sv) * prm.scale_log2);
                     fused = !__any_sync(0xffffffffu, !(bound <= m_ref + kFusedAbove));
                 }
@@ -603,11 +636,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if constexpr (kCap) cap_scores(prm.mod, sv);
                 if constexpr (kBias) {
                     // the distances t - u are exact in fp32 (below 2^24; relative to that beyond)
-                    const float base = static_cast<float>(q_local - kv0);
+                    const float base = static_cast<float>(q_dist - kv0);
                     const float bias = kCap ? bias2 : bias2 / prm.scale_log2;
-                    if (two_sided && j >= qt) {
+                    if ((two_sided && j >= qt) || prefix_end) {
+                        const float own = static_cast<float>(q_local - kv0);
 #pragma unroll
-                        for (int e = 0; e < 128; ++e) sv[e] = fmaf(fabsf(base - e), bias, sv[e]);
+                        for (int e = 0; e < 128; ++e)
+                            sv[e] = fmaf(fabsf((kPositions && kv0 + e >= P ? own : base) - e), bias, sv[e]);
                     } else {
                         const float2 b2 = make_float2(base, base), s2 = make_float2(bias, bias);
 #pragma unroll
@@ -668,7 +703,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float to_log2 = kCap ? 1.f : prm.scale_log2;
             const float2 sc2 = make_float2(to_log2, to_log2);
             const float2 nm2 = make_float2(neg_m, neg_m);
-            const float fused_base = kBias ? fmaf(static_cast<float>(q_local - kv0), bias2, neg_m) : neg_m;
+            const float fused_base = kBias ? fmaf(static_cast<float>(q_dist - kv0), bias2, neg_m) : neg_m;
             auto exps = [&](int c, float (&p)[32], auto fuse) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {

@@ -1,7 +1,8 @@
 // Modified scores: what the attention kernels do to S = <q_t, k_u> between the two matrix
 // products.  In units of log2 (the softmax runs in the exp2 domain), with s2 = scale log2 e:
 //   y = C tanh(S a), a = scale / cap, C = cap log2 e       (kCap; else y = S s2)
-//   z = y - slope_h log2(e) |t - u|                        (kBias)
+//   z = y - slope_h log2(e) |t - u|                        (kBias; kPositions: position_t - u to
+//                                                           prefix keys u)
 //   z = -inf unless the mask lets row t see key u          (kMask)
 // and in the gradient dy = P (dP - D), dS = dy (1 - (y / C)^2) scale.
 //
@@ -15,7 +16,7 @@
 
 namespace lf {
 
-enum { kModCap = 1, kModBias = 2, kModMask = 4 };
+enum { kModCap = 1, kModBias = 2, kModMask = 4, kModPositions = 8 };   // the last with kModBias | kModMask only
 
 // tanh(x) = x p(x^2), p a relative minimax fit (iterated weighted least squares on Chebyshev
 // nodes, in double).  tanh.approx (2^-11) would cost the scores three digits, and exp and a
@@ -155,6 +156,10 @@ __device__ __forceinline__ int prefix_of(const ModParams& m, int s, int len, boo
     bad = p < 0;
     return min(max(p, 0), len);
 }
+
+// Row t's position within its bounds: the distance to the prefix keys that it sees, u < P and
+// u <= t, is then never negative, nor more than that in rows.
+__device__ __forceinline__ int bounded_position(int pos, int t, int P) { return min(max(pos, min(t, P - 1)), t); }
 
 // The KV tiles that a pair of query tiles (2m, 2m+1) needs, in ascending order: slot i is KV
 // tile i for i < n_prefix, then lo, lo + 1, ...  The forward takes the slots from the last to

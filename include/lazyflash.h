@@ -231,6 +231,8 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
  *
  *   z(t, u) = cap(softmax_scale * <q_t, k_u>) - slope_h * |t - u|,
  *   cap(x) = softcap * tanh(x / softcap),  and -inf where row t does not see key u.
+ *   |t - u| counts rows of the packed segment; with `positions` the distance to a prefix
+ *   key u < prefix_len[s] is positions[t] - u instead.
  *
  * Rows and keys are counted from their segment's start.  Row t sees
  *   its own keys     row_start[t] <= u <= t   (without row_start: u <= t), and
@@ -241,16 +243,22 @@ lf_status lf_attn_bwd_static_ws(const lf_attn_desc* desc, const void* q, const v
  * prompt of P tokens followed by its answers, row_start[t] = start of t's answer (0 in the
  * prompt), prefix_len = P, prefix_causal = 1, is a batch that shares its prompt: the
  * prompt's rows, K and V are computed once, and its dK and dV gather all answers' gradients.
+ * With alibi_slopes such a batch needs `positions` (P plus the row's index in its answer; in
+ * the prompt the row itself): without, an answer's distance to its prompt includes the rows of
+ * the answers packed in between, which is not what a copy of the prompt for each would give.
  * ------------------------------------------------------------------------- */
 typedef struct {
     float softcap;               /* 0: none; else in [1e-3, 1e6] */
     const float* alibi_slopes;   /* DEVICE [hq], finite, of either sign, or NULL: no bias.  No gradient is
-                                    computed for it.  The distance counts rows of the packed segment */
+                                    computed for it */
     const int32_t* prefix_len;   /* DEVICE [nseq], >= 0 (beyond the segment: the whole segment), or NULL */
     int32_t prefix_causal;       /* 0 or 1 (1 only with prefix_len) */
     const int32_t* row_start;    /* DEVICE [total_tokens], or NULL.  Within a segment 0 <= row_start[t] <= t,
                                     and it never decreases: every row sees itself.  Not read outside
                                     segments */
+    const int32_t* positions;    /* DEVICE [total_tokens], or NULL; only with prefix_causal.  Within a
+                                    segment min(t, prefix_len - 1) <= positions[t] <= t.  Read where
+                                    there are slopes, not outside segments */
 } lf_score_mod;
 
 /* lf_attn_fwd and lf_attn_bwd with modified scores.  Arguments, results, workspace
