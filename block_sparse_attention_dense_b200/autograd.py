@@ -117,7 +117,12 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     lf_score_mod in include/lazyflash.h says how, shared_prompt_tables makes the last's.  The
     bias counts rows of the packed segment: answers that share a prompt need ``positions`` [T]
     (the table's fourth) as well, from which it then counts the distance to the prompt's keys;
-    without, an answer is too far from its prompt by the answers packed before it."""
+    without, an answer is too far from its prompt by the answers packed before it.  With
+    modified scores the backward also keeps O's rounding residual, a second tensor of O's size
+    (no gradient asked for: not allocated).
+
+    Every row belongs to a segment (cu_seqlens[-1] = T): rows behind the last one are left
+    unwritten in the result and the gradients."""
     if alibi_slopes is not None and alibi_slopes.requires_grad and torch.is_grad_enabled():
         raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,

@@ -18,7 +18,8 @@
 // Per half:
 //   tcgen05 (SS): S^T  = K_j Q_h^T,  dP^T = V_j dO_h^T        (TMEM, fp32)
 //   element-wise: P = exp2(S*scale*log2e - LSE*log2e), dS = P (dP - D), both
-//                 times the block weight; P^T and dS^T rounded to bf16 back
+//                 times the block weight; P^T and dS^T rounded to bf16 (the type
+//                 in which the tensor core takes them; all sums are fp32) back
 //                 into TMEM (both over S^T) and dS^T into shared memory
 //   tcgen05 (SS): dQ_h^T = K_j^T dS^T_h       (TMEM, over dP^T; lanes = d)
 //   tcgen05 (TS): dV_j += P^T dO_h, dK_j += dS^T Q_h   (A from TMEM)
@@ -44,8 +45,12 @@
 // CTA visits only the kept query tiles between the first row that may see its keys and the
 // last one that does; within them, the rows that see a key are one run, so that a thread
 // (one key) compares the query's index with two bounds, and not at all in halves that hide
-// nothing.  16,384 tokens, 32/8 heads of 128, causal, 30 % of the blocks kept, plain
-// 1.92 ms: cap 2.27, bias 1.97, a mask that hides nothing 2.16, a window of 1,024 keys 0.50.
+// nothing.  Where distances to prefix keys are counted from positions (kModPositions), those
+// keys read the columns' part of the bias from a vector of their own.
+// 16,384 tokens, 32/8 heads of 128, causal, 30 % of the blocks kept, ms in short runs (in
+// brackets back to back, under the power cap): plain 1.92 (2.16), cap 50 2.20 (2.43), bias 1.88
+// (2.02), a mask that hides nothing 1.93 (2.14), cap and bias 2.36 (2.42), a window of 1,024
+// keys 0.47 (0.43).
 //
 // Tensor memory (512 columns): dV [0,128) dK [128,256); half 0: S^T [256,320)
 // (after the element-wise pass: P^T in its first 32 columns, dS^T in the next 32,

@@ -33,11 +33,13 @@
 // (kModPositions: a shared prompt's answers): a row's distances then have another start in the
 // prefix's tiles, and in the one tile at the prefix's end a start per key.  A variant of its
 // own, as the same code behind a runtime test made the biased masks 2-3 % slower.
-// A row's softmax warp is bound by its own latency (the exp2 unit
-// and the FMA pipes are busy 45 and 36 % of the time under a cap), so the cap and the bias
-// are laid beside the exp2 (capped_row; `fused`).  16,384 tokens, 32/8 heads of 128, causal,
-// plain 1.72 ms: cap 2.36, bias 1.86, a mask that hides nothing 1.87, both cap and bias
-// 2.9-3.1, a window of 1,024 keys 0.45 ms.
+// A row's softmax warp is bound by its own latency (under a cap the exp2 unit is busy 40 % of
+// the time and the FMA pipes 23 %), so the cap and the bias are laid beside the exp2
+// (capped_row; `fused`).  16,384 tokens, 32/8 heads of 128, causal, scores of deviation 2, ms in
+// short runs (in brackets back to back, under the power cap): plain 1.76 (1.97), cap 50 2.29
+// (2.51), cap 100, which keeps the running maximum, 2.74 (2.90), bias 2.00 (2.15), a mask that
+// hides nothing 1.83 (2.05), cap and bias 2.45 (2.60), a window of 1,024 keys 0.45 (0.42).
+// P is rounded to bf16, the type in which the tensor core takes it beside V; its sums stay in fp32.
 #pragma once
 
 #include <climits>
@@ -58,7 +60,8 @@ struct FwdParams {
 };
 struct FwdModParams : FwdParams {
     ModParams mod;
-    __nv_bfloat16* o_low;      // [T][hq][D] what rounding took from o, or null
+    __nv_bfloat16* o_low;      // [T][hq][D] what rounding took from o, or null (bf16: 16 bits of O
+                               // in all, which leaves D no error beside that of P's rounding)
 };
 struct FwdPositionsParams : FwdModParams {
     const int32_t* positions;  // [T] where distances to prefix keys are counted from

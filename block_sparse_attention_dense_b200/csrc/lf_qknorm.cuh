@@ -117,7 +117,7 @@ template <bool kPairs>
 struct LaneAngles {
     Four ca, sa;   // of chunk A
     Four cb, sb;   // of chunk B (kPairs; halves share the cosines and negate the sines)
-    // kBack: the opposite angle
+    // back: the opposite angle
     __device__ void load(const float* row, int l, int rot, bool on, bool back) {
         const float sg = back ? -1.f : 1.f;
         const float2 one = make_float2(1.f, 1.f);
@@ -173,7 +173,7 @@ __device__ __forceinline__ int token_position(const QkParams& p, int t, int t_en
     return bad ? -1 : pos;
 }
 
-// One kind of head (q or k) of a token: row groups [g0, g1), kRpw rows each.
+// One kind of head (q or k) of a token: row groups [g0, g1) of 32 / (D / 8) rows each.
 struct QkRows {
     const __nv_bfloat16* x;   // this lane's row 0 (token and lane's sub-row applied)
     const __nv_bfloat16* g;
