@@ -858,9 +858,9 @@ lf_status lf_qk_norm_rope_bwd(const lf_qk_desc* desc, const void* q, int64_t q_s
     p.oks = dk_stride;
     p.partial = weights ? static_cast<float*>(ws) : nullptr;
     // lanes that hold no row (a surplus head, a row behind the last segment) hold zeros: with
-    // eps = 0 their root would be inf, and 0 * inf reach the weights' sums.  The least normal
-    // number changes no row whose squares' mean is above 1e-30 (a test per row cost 2 %)
-    p.eps = std::max(p.eps, std::numeric_limits<float>::min());
+    // eps = 0 their root would be inf, and 0 * inf reach the weights' sums.  The least number
+    // above 0 keeps it finite and is lost beside any row's mean square (a test per row cost 2 %)
+    if (p.eps == 0.f) p.eps = std::numeric_limits<float>::denorm_min();
     const int blocks = qk_grid(desc, p, true);
     if ((st = launch_qk_any(desc, p, blocks, true, s)) != LF_OK) return st;
     if (weights) {

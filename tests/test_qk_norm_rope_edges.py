@@ -51,6 +51,29 @@ def test_weight_gradients_without_eps(c):
         assert torch.equal(w.grad, dw.to(w.dtype))
 
 
+@gpu
+def test_rows_of_tiny_values_without_eps():
+    """Squares near the least normal number, 2^-126: nothing but the row's own mean square counts.
+    Each square is off by half of 2^-149 at most, 2^-143 for 128 of them, which is 2^-28 of their
+    sum: less than one rounding."""
+    c = Case("tiny", (40,), 4, 2, 128, 128)
+    m = c.make(12)
+    gen = torch.Generator().manual_seed(2)
+    m["qkv"].copy_(torch.randn(m["qkv"].shape, generator=gen) * 2.0 ** -61)
+    g = c.dev(m)
+    cs = cs_rows(c, m)
+    desc = c.desc(g, eps=0.0)
+    dq, dk = torch.empty_like(g["dyq"]), torch.empty_like(g["dyk"])
+    dqw, dkw = torch.empty(2, c.d, device="cuda")
+    ws = torch.empty(lf.lf_qk_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    lf.lf_qk_norm_rope_bwd(desc, g["q"], g["k"], g["dyq"], g["dyk"], dq, dk, dqw, dkw, ws)
+    lf.lf_sync_status()
+    for x, w, dy, dx, dw in ((m["q"], m["qw"], m["dyq"], dq, dqw), (m["k"], m["kw"], m["dyk"], dk, dkw)):
+        ref, size, rdw, wsize = ref_backward(x, w, cs, c.rot, c.interleaved, 0.0, True, dy)
+        check_dx(ref, size, dx, m["T"])
+        assert ((dw.cpu().double() - rdw).abs() <= (256 + 32) * U * wsize).all()
+
+
 def test_a_table_that_asks_for_a_gradient_is_refused():
     q, k = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
     table = lf.rope_cos_sin(8, 64, device="cpu").requires_grad_(True)
