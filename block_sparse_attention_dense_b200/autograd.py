@@ -27,13 +27,9 @@ from . import (Buffers, lf_attn_bwd, lf_attn_bwd_mod, lf_attn_fwd, lf_attn_fwd_m
 _step_counter = itertools.count()
 
 
-def _score_mod(softcap, prefix_causal, *arrays):
-    """The modifier of the scores, or None for the plain attention; arrays: alibi_slopes,
-    prefix_len, row_start, positions."""
-    if softcap or prefix_causal or any(a is not None for a in arrays):
-        alibi_slopes, prefix_len, row_start, positions = arrays
-        return make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions)
-    return None
+def _modified(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions):
+    return bool(softcap or prefix_causal or alibi_slopes is not None or prefix_len is not None
+                or row_start is not None or positions is not None)
 
 
 class LazyFlashAttention(torch.autograd.Function):
@@ -50,21 +46,18 @@ class LazyFlashAttention(torch.autograd.Function):
         desc = make_desc(cu_seqlens, max_seqlen, T, hq, hkv, d, scale, causal, block_q)
         o = torch.empty_like(q)
         lse = torch.empty(hq, T, dtype=torch.float32, device=q.device)
-        o_low = None
-        arrays = (alibi_slopes, prefix_len, row_start, positions)
-        mod = _score_mod(softcap, prefix_causal, *arrays)
-        if mod is None:
-            lf_attn_fwd(desc, q, k, v, o, lse)
-        else:
+        if _modified(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions):
+            mod = make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions)
             # O's rounding residual, kept for the backward's D (not when no gradient is asked for)
-            if any(ctx.needs_input_grad):
-                o_low = torch.empty_like(q)
+            o_low = torch.empty_like(q) if any(ctx.needs_input_grad) else None
             lf_attn_fwd_mod(desc, mod, q, k, v, o, lse, o_low)
-        # the modifier's arrays are saved as cu_seqlens is, so that one written to between the two
-        # passes is noticed: P comes from this pass's LSE and the backward's own scores
-        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low, *arrays)
-        ctx.softcap = softcap
-        ctx.prefix_causal = prefix_causal
+            # the modifier's arrays are saved as cu_seqlens is, so that one written to between the
+            # two passes is noticed: P comes from this pass's LSE and the backward's own scores
+            ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, o_low, alibi_slopes, prefix_len, row_start, positions)
+            ctx.scalars = (softcap, prefix_causal)
+        else:
+            lf_attn_fwd(desc, q, k, v, o, lse)
+            ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
         ctx.desc = desc
         ctx.delta = float(delta)
         ctx.seed = int(seed)
@@ -74,9 +67,13 @@ class LazyFlashAttention(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_o):
-        q, k, v, o, lse, cu_seqlens, o_low, *arrays = ctx.saved_tensors
+        q, k, v, o, lse, cu_seqlens, *modifier = ctx.saved_tensors
         desc = ctx.desc
-        mod = _score_mod(ctx.softcap, ctx.prefix_causal, *arrays)
+        mod = None
+        if modifier:
+            o_low, alibi_slopes, prefix_len, row_start, positions = modifier
+            softcap, prefix_causal = ctx.scalars
+            mod = make_score_mod(softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions)
         dout = grad_o.to(torch.bfloat16).contiguous()
         # the backward's own buffers only: o and lse are the forward's saved tensors
         bufs = Buffers(desc, device=q.device, forward=False)
@@ -125,9 +122,9 @@ def lazyflash_attention(q, k, v, cu_seqlens, max_seqlen, delta=0.1, seed=0, step
     unwritten in the result and the gradients."""
     if alibi_slopes is not None and alibi_slopes.requires_grad and torch.is_grad_enabled():
         raise ValueError("no gradient is computed for alibi_slopes: pass them detached")
+    modifier = (softcap, alibi_slopes, prefix_len, prefix_causal, row_start, positions)
     return LazyFlashAttention.apply(q, k, v, cu_seqlens, max_seqlen, delta, seed, step, causal,
-                                    block_q, softmax_scale, selection_out, softcap, alibi_slopes, prefix_len,
-                                    prefix_causal, row_start, positions)
+                                    block_q, softmax_scale, selection_out, *(modifier if _modified(*modifier) else ()))
 
 
 class QkNormRope(torch.autograd.Function):
